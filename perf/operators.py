@@ -1,0 +1,447 @@
+"""Cases of the paged key/value cache: appending rotated keys and values (16 or 4 bits a value),
+attention over the cache (sliding window with visible first tokens, whole contexts, selected
+keys), and the contiguous sliding-window attention with visible first tokens.
+
+A cache row holds one token: [K | V] in bf16, or in 4 bits [K codes | V codes | K scales | V
+scales], padded to 16 bytes.  Codes are e2m1, two to a byte (even element in the low half), and
+every 16 elements of a head share an e4m3 scale; a tensor-wide float32 scale multiplies them.
+"""
+import math
+
+import torch
+
+own = False
+
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+BF = torch.bfloat16
+
+
+# ------------------------------------------------------------------------------------ cases
+def _case(name, op, **kw):
+    c = dict(op=op, B=1, S=1, H=32, HKV=8, DQK=192, DV=128, fmt="e2m1", page=64, ctx=0, window=0,
+             first=0, K=0, gate=False, rope="interleaved", k_scale=1.0)
+    c.update(kw)
+    if name:
+        c["name"] = name
+    return c
+
+
+def listed():
+    return [
+        # one decode step's new tokens of 64 sequences into a 4-bit cache, queries rotated too
+        _case("append_decode", "append", B=64, ctx=9000),
+        # two prompts of odd length, 4 bits, half-split rotation, a tensor-wide key scale
+        _case("append_prompt_4bit", "append", B=2, S=4001, ctx=4001, rope="half", k_scale=0.5),
+        # a long prompt with 32 key/value heads kept in bf16
+        _case("append_prompt_bf16", "append", S=8192, ctx=8192, HKV=32, fmt="bf16"),
+        # sliding-window layers on prompts: 20 equal heads; ragged batch behind a cached prefix
+        # (queries are the last S of ctx tokens); the hybrid block's layer at 32768 tokens
+        _case("window_prompt", "window", S=4096, ctx=4096, H=20, HKV=20, DQK=128, window=512,
+              first=4),
+        _case("window_ragged", "window", B=3, S=1000, ctx=1777, window=300, first=17, gate=True),
+        _case("window_long", "window", S=32768, ctx=32768, window=512, first=128, gate=True),
+        # one sequence, one token: nothing but latency
+        _case("cache_window_one", "cache", ctx=4100, window=512, first=4),
+        # a decode step of a sliding-window layer for 64 sequences of different lengths
+        _case("cache_window_batch", "cache", B=64, ctx=8192, window=512, first=4, fmt="bf16",
+              gate=True),
+        # whole contexts of up to 131072 tokens in 4 bits, grouped heads
+        _case("cache_full_long", "cache", B=8, ctx=131072),
+        # selected keys, 32 expanded heads: the sparse decode step over a 4-bit cache
+        _case("cache_sparse_decode", "sparse", B=64, HKV=32, ctx=8192, K=2048),
+        # the same over bf16 rows, fewer sequences, gated
+        _case("cache_sparse_bf16", "sparse", B=16, HKV=32, ctx=8192, K=2048, fmt="bf16",
+              gate=True),
+        # four draft tokens of each of five sequences, pages of 48 tokens
+        _case("cache_sparse_draft", "sparse", B=5, S=4, H=20, HKV=20, DQK=128, ctx=3001, K=512,
+              page=48),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("append", "window", "cache", "sparse"))
+    H, HKV = rng.choice(((32, 8), (32, 32), (20, 20), (16, 2), (8, 1), (4, 4), (24, 8), (32, 1)))
+    c = dict(H=H, HKV=HKV, DQK=rng.choice((64, 128, 192)), DV=rng.choice((64, 128)),
+             fmt=rng.choice(("e2m1", "bf16")), page=rng.choice((16, 48, 64, 100, 128)),
+             gate=rng.random() < 0.5, rope=rng.choice(("interleaved", "half", "off")),
+             k_scale=rng.choice((0.25, 1.0, 2.0)))
+    if op == "append":
+        c["B"] = _log(rng, 1, 64)
+        c["S"] = rng.choice((1, _log(rng, 1, max(1, 8192 // c["B"]))))
+        c["ctx"] = c["S"] + _log(rng, 1, 9000)
+    elif op == "window":
+        c.update(DQK=rng.choice((128, 192)), DV=128, B=_log(rng, 1, 4), window=_log(rng, 16, 512))
+        c["S"] = _log(rng, 64, 16384 // c["B"])
+        c["ctx"] = c["S"] + rng.choice((0, _log(rng, 1, 1000)))
+        c["first"] = rng.randint(1, 128)
+    else:
+        c["B"] = _log(rng, 1, 64)
+        c["S"] = rng.choice((1, 1, rng.randint(2, 4)))
+        c["ctx"] = _log(rng, 2 + c["S"], 8192)
+        if op == "sparse":
+            c["K"] = _log(rng, 1, 2048)
+        elif rng.random() < 0.6:
+            c["window"], c["first"] = _log(rng, 1, 512), rng.randint(0, 64)
+        else:
+            c["B"] = min(c["B"], 16)
+    return _case("", op, **c)
+
+
+# ------------------------------------------------------------------------------------ 4 bits
+def _encode(x, scale):
+    """x [..., D] bf16 -> codes [..., D/2] and scales [..., D/16], uint8: y = x / scale, a group's
+    scale is its largest |y| / 6 in e4m3, an element's code y / scale in e2m1, both rounded to
+    nearest even and saturated; each operation in float32."""
+    y = (x.float() / scale).unflatten(-1, (-1, 16))
+    amax = y.abs().amax(-1)
+    s = (amax / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    z = y / s.float().unsqueeze(-1)
+    z = torch.where(s.float().unsqueeze(-1) == 0, torch.zeros_like(z), z)
+    m = z.abs()
+    # the code is the number of borders passed; a tie goes to the even code
+    code = torch.zeros_like(m, dtype=torch.uint8)
+    for border, even_below in ((0.25, True), (0.75, False), (1.25, True), (1.75, False),
+                               (2.5, True), (3.5, False), (5.0, True)):
+        code += (m > border if even_below else m >= border).to(torch.uint8)
+    code += torch.signbit(z).to(torch.uint8) * 8
+    code = code.flatten(-2)
+    return code[..., 0::2] | (code[..., 1::2] << 4), s.view(torch.uint8)
+
+
+def _decode(codes, scales, scale):
+    """The float32 values that codes and scales stand for."""
+    table = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=codes.device)
+    v = table[torch.stack((codes & 15, codes >> 4), -1).flatten(-2).int()]
+    s = scales.view(torch.float8_e4m3fn).float()
+    return (v.unflatten(-1, (-1, 16)) * s.unsqueeze(-1)).flatten(-2) * scale
+
+
+def _row_bytes(c):
+    n = c["HKV"] * (c["DQK"] + c["DV"])
+    return 2 * n if c["fmt"] == "bf16" else (n // 2 + n // 16 + 15) // 16 * 16
+
+
+def _pack(c, k, v):
+    """Rows [n, row] as the cache holds them, of k [n, HKV, DQK] and v [n, HKV, DV]."""
+    if c["fmt"] == "bf16":
+        return torch.cat((k.flatten(1), v.flatten(1)), 1)
+    (kc, ks), (vc, vs) = _encode(k, c["k_scale"]), _encode(v, 1.0)
+    row = torch.cat([t.flatten(1) for t in (kc, vc, ks, vs)], 1)
+    return torch.nn.functional.pad(row, (0, _row_bytes(c) - row.shape[1]))
+
+
+def _unpack(c, rows):
+    """(k [..., HKV, DQK], v [..., HKV, DV]) in float32 of rows [..., row]."""
+    nk, nv = c["HKV"] * c["DQK"], c["HKV"] * c["DV"]
+    if c["fmt"] == "bf16":
+        k, v = rows.float().split((nk, nv), -1)
+    else:
+        kc, vc, ks, vs = rows[..., : (nk + nv) // 16 * 9].split(
+            (nk // 2, nv // 2, nk // 16, nv // 16), -1)
+        k, v = _decode(kc, ks.contiguous(), c["k_scale"]), _decode(vc, vs.contiguous(), 1.0)
+    return k.unflatten(-1, (c["HKV"], c["DQK"])), v.unflatten(-1, (c["HKV"], c["DV"]))
+
+
+# ------------------------------------------------------------------------------------ inputs
+def prepare(case, seed):
+    c, dev = case, torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+    n01 = lambda *shape: torch.randn(*shape, device=dev, generator=g, dtype=torch.float32).to(BF)  # noqa: E731
+    B, S, H, HKV, ctx = c["B"], c["S"], c["H"], c["HKV"], c["ctx"]
+    st = {"case": c}
+    if c["gate"]:
+        st["gate"] = n01(B, S, H)
+    st["q"] = n01(B, S, H, c["DQK"])
+    if c["op"] == "window":
+        st["k"], st["v"] = n01(B, ctx, HKV, c["DQK"]), n01(B, ctx, HKV, c["DV"])
+        return st
+    # contexts of different lengths, the first the longest; pages in a shuffled order
+    lens = torch.randint(max(S, ctx // 2), ctx + 1, (B,), device=dev, generator=g)
+    lens[0] = ctx
+    st["pos"] = (lens[:, None] - S + torch.arange(S, device=dev)).int()
+    pages_each = -(-ctx // c["page"])
+    n_pages = B * pages_each + 3
+    order = torch.randperm(n_pages, device=dev, generator=g)
+    st["table"] = order[: B * pages_each].view(B, pages_each).int().contiguous()
+    row = _row_bytes(c)
+    st["pages"] = torch.zeros(n_pages, c["page"], row // 2 if c["fmt"] == "bf16" else row,
+                              dtype=BF if c["fmt"] == "bf16" else torch.uint8, device=dev)
+    if c["op"] == "append":
+        st["k"], st["v"] = n01(B, S, HKV, c["DQK"]), n01(B, S, HKV, c["DV"])
+        st["inv_freq"] = 10000.0 ** (-torch.arange(32, device=dev, dtype=torch.float32) / 32)
+    else:
+        flat = st["pages"].flatten(0, 1)
+        step = 1 << 16
+        for i in range(0, flat.shape[0], step):
+            n = min(step, flat.shape[0] - i)
+            flat[i : i + n] = _pack(c, n01(n, HKV, c["DQK"]), n01(n, HKV, c["DV"]))
+    if c["op"] == "sparse":
+        # min(K, visible keys) distinct visible keys of each query, ascending, then -1
+        K, p = c["K"], st["pos"].long().view(B * S, 1)
+        r = torch.rand(B * S, ctx, device=dev, generator=g)
+        r = torch.where(torch.arange(ctx, device=dev) <= p, r, 2.0 + r)
+        kept = r.topk(min(K, ctx), largest=False).indices
+        kept = torch.where(kept <= p, kept, ctx).sort().values
+        kept = torch.nn.functional.pad(kept, (0, K - kept.shape[1]), value=ctx)
+        st["idx"] = torch.where(kept < ctx, kept, -1).int().view(B, S, K).contiguous()
+    if own:
+        import sparse_attention_15_b200 as dsa
+
+        st["cache"] = dsa.Cache(st["pages"], st["table"], HKV, c["DQK"], c["DV"],
+                                k_scale=c["k_scale"])
+    return st
+
+
+# ------------------------------------------------------------------------------------ plain
+def _rows_at(st, t):
+    """The cache rows of keys t [B, ...] (each in its sequence's range)."""
+    c = st["case"]
+    b = torch.arange(t.shape[0], device=t.device).view(-1, *[1] * (t.dim() - 1))
+    phys = st["table"].long()[b, t // c["page"]] * c["page"] + t % c["page"]
+    return phys
+
+
+def _rotate(x, pos, inv_freq, mode):
+    """The last 2 * len(inv_freq) dims of x [B, S, n, D] rotated by pos * inv_freq, in float64 (the
+    angles of far positions need it), rounded through float32 to bf16."""
+    if mode == "off":
+        return x
+    r = 2 * inv_freq.numel()
+    a = (pos.double()[..., None] * inv_freq.double())[:, :, None, :]
+    co, si = a.cos(), a.sin()
+    keep, y = x[..., :-r], x[..., -r:].double()
+    if mode == "interleaved":
+        u, w = y[..., 0::2], y[..., 1::2]
+        y = torch.stack((u * co - w * si, w * co + u * si), -1).flatten(-2)
+    else:
+        u, w = y[..., : r // 2], y[..., r // 2 :]
+        y = torch.cat((u * co - w * si, w * co + u * si), -1)
+    return torch.cat((keep, y.float().to(BF)), -1)
+
+
+def _gated(c, st, o):
+    return o * torch.sigmoid(st["gate"].float())[..., None] if c["gate"] else o
+
+
+def _attend(c, q, k, v, seen):
+    """q [.., n, HKV, g, DQK], k [.., m, HKV, DQK], v [.., m, HKV, DV], seen [.., n, m] -> [.., n,
+    HKV, g, DV]: softmax over the seen keys, zeros where there are none."""
+    s = torch.einsum("...nhgd,...mhd->...hgnm", q, k) / math.sqrt(c["DQK"])
+    s = s.masked_fill(~seen[..., None, None, :, :], -math.inf)
+    top = s.amax(-1, keepdim=True)
+    p = (s - torch.where(top == -math.inf, 0.0, top)).exp()
+    o = torch.einsum("...hgnm,...mhd->...nhgd", p, v)
+    return o / p.sum(-1).clamp(min=1e-30).movedim(-1, -3)[..., None]
+
+
+def _plain_append(st):
+    c, pos = st["case"], st["pos"]
+    q = _rotate(st["q"], pos, st["inv_freq"], c["rope"])
+    k = _rotate(st["k"], pos, st["inv_freq"], c["rope"])
+    at = _rows_at(st, pos.long()).flatten()
+    flat = st["pages"].flatten(0, 1)
+    flat[at] = _pack(c, k.flatten(0, 1), st["v"].flatten(0, 1))
+    kv = _unpack(c, flat[at])
+    return [q] + [x.to(BF).unflatten(0, pos.shape) for x in kv]
+
+
+def _plain_window(st):
+    # query blocks of W tokens against their own and the previous key block, and the first tokens
+    c = st["case"]
+    B, S, H, HKV, T, W, F = (c[n] for n in ("B", "S", "H", "HKV", "ctx", "window", "first"))
+    off, dev = T - S, st["q"].device
+    W2 = max(W, 64)
+    n = -(-T // W2)
+    pad = lambda x, lo: torch.nn.functional.pad(x.float(), (0, 0, 0, 0, lo, n * W2 - T))  # noqa: E731
+    q = pad(st["q"], off).view(B, n, W2, HKV, H // HKV, c["DQK"])
+    k, v = (pad(st[x], W2).unflatten(1, (n + 1, W2)) for x in "kv")
+    k, v = (torch.cat((x[:, :-1], x[:, 1:]), 2) for x in (k, v))
+    F = min(F, T)
+    fk, fv = (st[x][:, None, :F].float().expand(-1, n, -1, -1, -1) for x in "kv")
+    i = torch.arange(n, device=dev)[:, None, None]
+    s = i * W2 + torch.arange(W2, device=dev)[None, :, None]
+    t = (i - 1) * W2 + torch.arange(2 * W2, device=dev)[None, None, :]
+    f = torch.arange(F, device=dev)[None, None, :]
+    seen = torch.cat(((f <= s - W), (t >= 0) & (t <= s) & (t > s - W)), -1)
+    o = _attend(c, q, torch.cat((fk, k), 2), torch.cat((fv, v), 2), seen)
+    o = o.reshape(B, n * W2, H, c["DV"])[:, off : off + S]
+    return _gated(c, st, o).to(BF)
+
+
+def _plain_cache(st):
+    c, pos = st["case"], st["pos"].long()
+    B, S, H, HKV = c["B"], c["S"], c["H"], c["HKV"]
+    q = st["q"].float().view(B, S, HKV, H // HKV, c["DQK"])
+    if c["op"] == "sparse":
+        t = st["idx"].long()
+        seen = t >= 0
+    else:
+        t = torch.arange(c["ctx"], device=q.device)
+        if c["window"]:
+            W, F = c["window"], min(c["first"], c["ctx"])
+            t = torch.cat((torch.arange(F, device=q.device).expand(B, S, F),
+                           pos[..., None] - W + 1 + torch.arange(W, device=q.device)), -1)
+            low = (pos[..., None] - W + 1).clamp(min=0)
+            seen = torch.cat((t[..., :F] < low, t[..., F:] >= 0), -1)
+        else:
+            t = t.expand(B, 1, -1)  # one reading of the context for all S queries
+            seen = t <= pos[..., None]
+    at = _rows_at(st, t.clamp(min=0))
+    k, v = _unpack(c, st["pages"].flatten(0, 1)[at])
+    if c["op"] == "cache" and not c["window"]:
+        o = _attend(c, q, k[:, 0], v[:, 0], seen)
+    else:
+        o = _attend(c, q[:, :, None], k, v, seen[:, :, None])[:, :, 0]
+    return _gated(c, st, o.reshape(B, S, H, c["DV"])).to(BF)
+
+
+def run(st):
+    c = st["case"]
+    if own:
+        import sparse_attention_15_b200 as dsa
+
+        if c["op"] == "append":
+            q, _ = dsa.dsa_cache_append(st["cache"], st["pos"], st["k"], st["v"], rope=c["rope"],
+                                        inv_freq=st["inv_freq"], q=st["q"])
+            k, v = dsa.dsa_cache_read(st["cache"], st["pos"])
+            return [q, k, v]
+        gate = st.get("gate")
+        if c["op"] == "window":
+            return dsa.dsa_window_attn(st["q"], st["k"], st["v"], c["window"], gate=gate,
+                                       n_first=c["first"])
+        if c["op"] == "sparse":
+            return dsa.dsa_cache_sparse_attn(st["q"], st["cache"], st["pos"], st["idx"], gate=gate)
+        return dsa.dsa_cache_attn(st["q"], st["cache"], st["pos"], window=c["window"],
+                                  n_first=c["first"], gate=gate)
+    return {"append": _plain_append, "window": _plain_window}.get(c["op"], _plain_cache)(st)
+
+
+# ------------------------------------------------------------------------------------ floors
+def work(case):
+    c = case
+    B, S, H, HKV, ctx, D = c["B"], c["S"], c["H"], c["HKV"], c["ctx"], c["DQK"] + c["DV"]
+    row = _row_bytes(c)
+    if c["op"] == "append":  # q in and out, k and v in, rows written and read back, k and v out
+        n = B * S
+        return {"bytes": n * (4 * H * c["DQK"] + 4 * HKV * D + 2 * row + 4), "flops": 0}
+    qo = B * S * H * 2 * D
+    if c["op"] == "window":
+        pairs = sum(min(p + 1, c["window"]) + min(max(0, p + 1 - c["window"]), c["first"])
+                    for p in range(ctx - S, ctx))
+        return {"bytes": qo + B * ctx * HKV * 2 * D, "flops": 2 * B * H * pairs * D}
+    mean = 0.5 * (max(S, ctx // 2) + ctx) if B > 1 else ctx  # contexts: from half of ctx up
+    keys = min(mean, c["K"] if c["op"] == "sparse" else
+               c["window"] + c["first"] if c["window"] else mean)
+    once = min(mean, keys * S if c["op"] == "sparse" else keys + S - 1)
+    idx = 4 * B * S * c["K"]
+    return {"bytes": qo + B * once * row + idx, "flops": 2 * B * S * H * keys * D}
+
+
+# ------------------------------------------------------------------------------------ 64 bits
+def _values64(c, st, at):
+    """k and v of cache rows at [n], in float64, decoded bit by bit."""
+    rows = st["pages"].flatten(0, 1)[at]
+    nk, nv = c["HKV"] * c["DQK"], c["HKV"] * c["DV"]
+    if c["fmt"] == "bf16":
+        x = rows.double()
+        k, v = x[:, :nk], x[:, nk:]
+    else:
+        def part(code_at, scale_at, n):
+            b = rows[:, code_at : code_at + n // 2].long()
+            code = torch.stack((b % 16, b // 16), 2).reshape(len(rows), n)
+            e, m = code // 2 % 4, code % 2
+            mag = torch.where(e == 0, 0.5 * m, (1 + 0.5 * m) * 2.0 ** (e - 1).double())
+            s = rows[:, scale_at : scale_at + n // 16].long()
+            se, sm = s // 8 % 16, s % 8
+            sv = torch.where(se == 0, sm * 2.0**-9, (8 + sm) * 2.0 ** (se - 10).double())
+            return torch.where(code >= 8, -mag, mag) * sv.repeat_interleave(16, 1)
+
+        k = part(0, (nk + nv) // 2, nk) * c["k_scale"]
+        v = part(nk // 2, (nk + nv) // 2 + nk // 16, nv)
+    return k.view(-1, c["HKV"], c["DQK"]), v.view(-1, c["HKV"], c["DV"])
+
+
+def _nearest64(x, scale):
+    """What the 4-bit form of x [..., D] stands for, by search over the representable values."""
+    y = (x.double() / scale).unflatten(-1, (-1, 16))
+    e4m3 = torch.tensor([i * 2.0**-9 for i in range(8)]
+                        + [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8)][:-1],
+                        dtype=torch.float64, device=x.device)
+    e2m1 = torch.tensor(E2M1, dtype=torch.float64, device=x.device)
+
+    def nearest(v, table):
+        hi = torch.searchsorted(table, v.contiguous()).clamp(1, len(table) - 1)
+        lo = hi - 1
+        a, b = v - table[lo], table[hi] - v
+        up = (b < a) | ((b == a) & (hi % 2 == 0))
+        return torch.where(up, table[hi], table[lo])
+
+    s = nearest(y.abs().amax(-1, keepdim=True) / 6, e4m3)
+    z = torch.where(s == 0, 0.0, y.abs() / s.clamp(min=2.0**-12))
+    return (torch.sign(y) * nearest(z, e2m1) * s).flatten(-2) * scale
+
+
+def exact(case, seed):
+    c = case
+    st = prepare(c, seed)
+    B, S, H, HKV = c["B"], c["S"], c["H"], c["HKV"]
+    G = H // HKV
+    if c["op"] == "append":
+        def turned(x):
+            y = x.double()
+            if c["rope"] == "off":
+                return y
+            z0 = x.shape[-1] - 64
+            ang = st["pos"].double()[:, :, None, None] * st["inv_freq"].double()
+            j = torch.arange(32, device=x.device)
+            i0, i1 = (z0 + 2 * j, z0 + 2 * j + 1) if c["rope"] == "interleaved" else (z0 + j, z0 + 32 + j)
+            z = torch.polar(torch.ones_like(ang), ang) * torch.complex(y[..., i0], y[..., i1])
+            y[..., i0], y[..., i1] = z.real, z.imag
+            return y
+
+        q, k, v = turned(st["q"]), turned(st["k"]), st["v"].double()
+        if c["fmt"] == "e2m1":  # the cache takes K as bf16 holds it
+            k, v = _nearest64(k.float().to(BF), c["k_scale"]), _nearest64(v, 1.0)
+        return [q, k, v]
+    scale = 1.0 / math.sqrt(c["DQK"])
+    outs = []
+    for b in range(B):
+        if c["op"] == "window":
+            k, v = st["k"][b].double(), st["v"][b].double()
+        got = []
+        span = 512 if c["op"] == "window" else 1
+        for s0 in range(0, S, span):
+            s1 = min(S, s0 + span)
+            if c["op"] == "window":
+                p = torch.arange(c["ctx"] - S + s0, c["ctx"] - S + s1, device=k.device)
+                lo = max(0, int(p[0]) - c["window"] + 1) if s0 or c["ctx"] > S else 0
+                t = torch.arange(lo, int(p[-1]) + 1, device=k.device)
+                if lo > 0:
+                    t = torch.cat((torch.arange(min(lo, c["first"]), device=k.device), t))
+                kk, vv = k[t], v[t]
+                see = (t <= p[:, None]) & ((t > p[:, None] - c["window"]) | (t < c["first"]))
+            else:
+                p = int(st["pos"][b, s0])
+                if c["op"] == "sparse":
+                    t = st["idx"][b, s0].long()
+                    t = t[t >= 0]
+                else:
+                    t = torch.arange(p + 1, device=st["q"].device)
+                    if c["window"]:
+                        t = t[(t > p - c["window"]) | (t < c["first"])]
+                at = st["table"][b].long()[t // c["page"]] * c["page"] + t % c["page"]
+                kk, vv = _values64(c, st, at)
+                see = torch.ones(1, len(t), dtype=torch.bool, device=t.device)
+            q = st["q"][b, s0:s1].double()
+            kk, vv = kk.permute(1, 2, 0), vv.transpose(0, 1)  # [HKV, DQK, n], [HKV, n, DV]
+            q = q.view(s1 - s0, HKV, G, -1).permute(1, 2, 0, 3).reshape(HKV, G * (s1 - s0), -1)
+            a = (q @ kk * scale).view(HKV, G, s1 - s0, -1)
+            a = a.masked_fill(~see, -math.inf).softmax(-1).reshape(HKV, G * (s1 - s0), -1)
+            got.append((a @ vv).view(HKV, G, s1 - s0, -1).permute(2, 0, 1, 3).reshape(s1 - s0, H, -1))
+        outs.append(torch.cat(got))
+    o = torch.stack(outs)
+    return o / (1 + torch.exp(-st["gate"].double()))[..., None] if c["gate"] else o
