@@ -192,7 +192,7 @@ def prepare(case, seed):
         import sparse_attention_15_b200 as dsa
 
         st["cache"] = dsa.Cache(st["pages"], st["table"], HKV, c["DQK"], c["DV"],
-                                k_scale=c["k_scale"])
+                                k_scale=c["k_scale"] if c["fmt"] == "e2m1" else 1.0)
     return st
 
 
