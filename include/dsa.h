@@ -380,6 +380,105 @@ dsa_status dsa_window_attn_sinks(dsa_dtype dtype, const void* q, const void* k, 
                                  int window, int B, int S, int T, int H, int HKV, int DQK,
                                  int DV, dsa_attn_algo algo, void* out, dsa_stream_t stream);
 
+/* The same with the sequence's first tokens visible as well: query s also sees the keys
+ * t < n_first with t <= s+q_off (0 <= n_first <= 128, else DSA_ERR_UNSUPPORTED).  A key in both
+ * sets counts once.  K and V must be finite: as in dsa_window_attn, the tensor-core tiles multiply
+ * the values of keys a query does not see by zero. */
+dsa_status dsa_window_attn_first(dsa_dtype dtype, const void* q, const void* k, const void* v,
+                                 int n_first, const void* gate, dsa_gate_mode gate_mode,
+                                 float sm_scale, int window, int B, int S, int T, int H, int HKV,
+                                 int DQK, int DV, dsa_attn_algo algo, void* out,
+                                 dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * 5. The paged key/value cache.  [AXK2] "使用注意事项小结" item 2: the cache holds the expanded
+ *    K/V of every token; at 32 heads that is 20 KB a token.  Here the tokens of a sequence lie in
+ *    pages that a table names, and a row may be held in 4 bits.
+ *
+ *   pages  [n_pages, page_size, row]   device memory of the caller, 16-byte aligned; a row (one
+ *          token) is dsa_cache_row_bytes bytes:
+ *            DSA_CACHE_BF16  [K: HKV x DQK | V: HKV x DV] bf16
+ *            DSA_CACHE_E2M1  [K codes | V codes | K scales | V scales], padded to 16 bytes.  A
+ *                            code is an e2m1 value (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign), two to
+ *                            a byte, the even element in the low half; 16 elements of a head
+ *                            share an e4m3 scale.  An element is code * scale * k_scale (v_scale).
+ *   table  [B, max_pages] int32        token t of sequence b is row t % page_size of page
+ *          table[b][t / page_size].  An entry outside [0, n_pages) is no page: its tokens are
+ *          not stored, and not seen by the attention.
+ *   pos    [B, S] int32 (the calls' argument) the token's position in its sequence, from 0; a
+ *          negative one marks padding.
+ *   k_scale, v_scale  > 0, finite: the 4-bit form's scale of the whole tensor (a power of two
+ *          keeps it exact); 1 with DSA_CACHE_BF16.
+ *   DQK in {64, 128, 192}, DV in {64, 128}, HKV <= 64, max_pages * page_size <= 2^30; everything
+ *   is bf16 outside the cache.
+ * --------------------------------------------------------------------------------- */
+typedef enum { DSA_CACHE_BF16 = 0, DSA_CACHE_E2M1 = 1 } dsa_cache_format;
+/* Pairs of the rotated dims: (2j, 2j+1), or (j, j + rope_dim/2). */
+typedef enum { DSA_ROPE_OFF = 0, DSA_ROPE_INTERLEAVED = 1, DSA_ROPE_HALF = 2 } dsa_rope_mode;
+typedef struct {
+  dsa_cache_format format;
+  int n_pages, page_size, max_pages;
+  int HKV, DQK, DV;
+  float k_scale, v_scale;
+  void* pages;
+  const int32_t* table;
+} dsa_cache;
+
+size_t dsa_cache_row_bytes(dsa_cache_format format, int HKV, int DQK, int DV);
+
+/* 5a. Appends the tokens k [B,S,HKV,DQK], v [B,S,HKV,DV] at pos, the keys rotated on the way, and
+ *    rotates the queries of the same tokens.
+ *
+ *   rope_mode, rope_dim, inv_freq [rope_dim/2] float32: the last rope_dim dims of each key and
+ *          query head are rotated by pos * inv_freq[j] ([DSV2] items 4-6: q/k heads are qk_nope +
+ *          qk_rope wide), in float64, rounded to float32 and then to bf16.  rope_dim is a multiple
+ *          of 32, at most DQK.  DSA_ROPE_OFF: rope_dim 0, inv_freq NULL, and no q.
+ *   q      [B,S,H,DQK] or NULL; q_out [B,S,H,DQK] out, may be q
+ *   k_out  [B,S,HKV,DQK] out: the rotated keys as well, or NULL; may be k
+ *   4-bit rows: y = x / k_scale (v_scale); a group's scale is e4m3(max|y| / 6), to nearest and at
+ *   most 448; a code is e2m1(y / scale), to nearest even and at most 6; each operation one float32
+ *   operation, x the (rotated) bf16 value.  A group with a NaN or an infinity reads back as NaN.
+ *   A padding token (pos < 0) is not stored and gets zeros in q_out and k_out; a token without a
+ *   page is rotated but not stored.  Rows of other tokens are left as they were.  Two tokens of one
+ *   call must not have the same place in the cache: what that row then holds is unspecified.
+ *   q_out and k_out may not overlap other arguments.
+ */
+dsa_status dsa_cache_append(const dsa_cache* cache, const int32_t* pos, const void* k,
+                            const void* v, dsa_rope_mode rope_mode, int rope_dim,
+                            const float* inv_freq, int B, int S, int H, const void* q, void* q_out,
+                            void* k_out, dsa_stream_t stream);
+/* 5b. Reads the tokens at pos back: k [B,S,HKV,DQK], v [B,S,HKV,DV] bf16 (4-bit rows: the element's
+ *    value rounded to bf16; exact where k_scale and v_scale are powers of two).  Zeros where the
+ *    cache has no row. */
+dsa_status dsa_cache_read(const dsa_cache* cache, const int32_t* pos, int B, int S, void* k,
+                          void* v, dsa_stream_t stream);
+
+/* 5c. Attention of the tokens q [B,S,H,DQK] at pos over the cache: of each sequence's whole context
+ *    (window == 0: keys t <= pos), or of a sliding window with visible first tokens (t <= pos and
+ *    t > pos - window or t < n_first).  Query head h reads KV head h / (H/HKV).  For decode: one or
+ *    a few tokens per sequence, each reading its own keys.
+ *
+ *   gate, gate_mode, sm_scale (<= 0: 1/sqrt(DQK)), out [B,S,H,DV]: as dsa_sparse_attn.  Keys a
+ *   query does not see are not read, whatever they hold.  A row without keys (padding, a context
+ *   without pages) gets zeros.  Every visible key must have been appended.
+ *   H <= 64; HKV a multiple of 4 above 16 with DSA_CACHE_E2M1.  Workspace (partial results of key
+ *   slices) from dsa_cache_attn_workspace_bytes; 0 -> NULL is fine.
+ */
+size_t dsa_cache_attn_workspace_bytes(const dsa_cache* cache, int B, int S, int H, int window,
+                                      int n_first);
+dsa_status dsa_cache_attn(const dsa_cache* cache, const void* q, const int32_t* pos, int window,
+                          int n_first, const void* gate, dsa_gate_mode gate_mode, float sm_scale,
+                          int B, int S, int H, void* out, void* ws, size_t ws_bytes,
+                          dsa_stream_t stream);
+/* 5d. The same over selected keys: idx [B,S,K] int32 as the top-k gives them (section 2); -1,
+ *    entries past pos and tokens without a page are skipped.  A row's valid entries must be
+ *    distinct. */
+size_t dsa_cache_sparse_attn_workspace_bytes(const dsa_cache* cache, int B, int S, int H, int K);
+dsa_status dsa_cache_sparse_attn(const dsa_cache* cache, const void* q, const int32_t* pos,
+                                 const int32_t* idx, int K, const void* gate,
+                                 dsa_gate_mode gate_mode, float sm_scale, int B, int S, int H,
+                                 void* out, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* ---------------------------------------------------------------------------------
  * dsa_sparse_attn without any workspace: for callers that cannot allocate device memory.
  * The pages have no counterpart of this call; it exists for embedding.

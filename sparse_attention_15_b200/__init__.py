@@ -19,7 +19,8 @@ __all__ = [
     "dsa_sparse_attn", "dsa_sparse_attn_sinks", "dsa_sparse_attn_workspace_bytes",
     "dsa_sparse_attn_algo", "dsa_forward",
     "dsa_forward_workspace_bytes",
-    "dsa_window_attn", "dsa_sparse_attn_noalloc", "dsa_device_status", "dsa_version",
+    "dsa_window_attn", "Cache", "dsa_cache_pages", "dsa_cache_row_bytes", "dsa_cache_append",
+    "dsa_cache_read", "dsa_cache_attn", "dsa_cache_sparse_attn", "dsa_sparse_attn_noalloc", "dsa_device_status", "dsa_version",
     "dsa_test_arm_wait_timeout", "dsa_test_topk_bucket_floor", "LIB_PATH",
 ]
 
@@ -31,6 +32,8 @@ GATE = {"off": 0, "sigmoid": 1, "silu": 2}
 ATTN_ALGO = {"auto": 0, "gather": 1, "masked_tile": 2}
 INDEXER = {"per_head": 0, "collapsed": 1, "fused": 2}
 ATTN_FORM = {"expanded": 0, "latent": 1}
+CACHE_FORMAT = {"bf16": 0, "e2m1": 1}
+ROPE = {"off": 0, "interleaved": 1, "half": 2}
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "timeout",
           5: "internal"}
 
@@ -56,6 +59,16 @@ class ForwardArgs(ctypes.Structure):
         ("index_dtype", ctypes.c_int), ("sink_k", ctypes.c_void_p), ("sink_v", ctypes.c_void_p),
         ("nsink", ctypes.c_int), ("attn_form", ctypes.c_int),
         ("topk_fallback_out", ctypes.c_void_p),
+    ]
+
+
+class CacheArgs(ctypes.Structure):
+    """Mirror of dsa_cache (include/dsa.h)."""
+    _fields_ = [
+        ("format", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("HKV", ctypes.c_int), ("DQK", ctypes.c_int),
+        ("DV", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
     ]
 
 
@@ -92,6 +105,18 @@ _SIGNATURES = {
                              _P, _P]),
     "dsa_window_attn_sinks": (_I, [_I, _P, _P, _P, _P, _P, _I, _P, _I, _F, _I, _I, _I, _I, _I,
                                    _I, _I, _I, _I, _P, _P]),
+    "dsa_window_attn_first": (_I, [_I, _P, _P, _P, _I, _P, _I, _F, _I, _I, _I, _I, _I, _I, _I,
+                                   _I, _I, _P, _P]),
+    "dsa_cache_row_bytes": (_Z, [_I, _I, _I, _I]),
+    "dsa_cache_append": (_I, [ctypes.POINTER(CacheArgs), _P, _P, _P, _I, _I, _P, _I, _I, _I, _P,
+                              _P, _P, _P]),
+    "dsa_cache_read": (_I, [ctypes.POINTER(CacheArgs), _P, _I, _I, _P, _P, _P]),
+    "dsa_cache_attn_workspace_bytes": (_Z, [ctypes.POINTER(CacheArgs), _I, _I, _I, _I, _I]),
+    "dsa_cache_attn": (_I, [ctypes.POINTER(CacheArgs), _P, _P, _I, _I, _P, _I, _F, _I, _I, _I, _P,
+                            _P, _Z, _P]),
+    "dsa_cache_sparse_attn_workspace_bytes": (_Z, [ctypes.POINTER(CacheArgs), _I, _I, _I, _I]),
+    "dsa_cache_sparse_attn": (_I, [ctypes.POINTER(CacheArgs), _P, _P, _P, _I, _P, _I, _F, _I, _I,
+                                   _I, _P, _P, _Z, _P]),
     "dsa_sparse_attn_noalloc_max_scratch_bytes": (_Z, []),
     "dsa_sparse_attn_noalloc": (_I, [_I, _P, _P, _P, _P, _I, _P, _I, _F, _I, _I, _I, _I, _I, _I,
                                      _P, _P]),
@@ -417,16 +442,24 @@ def dsa_forward(q_idx, k_idx, w, index_scale, K, q, k, v, gate=None, gate_mode=N
 
 
 def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, algo="auto",
-                    out=None, stream=None, sink_k=None, sink_v=None):
+                    out=None, stream=None, sink_k=None, sink_v=None, n_first=0):
     """Sliding-window causal attention with grouped KV heads (window keys incl. self);
-    optional attention sinks sink_k [NS,HKV,DQK], sink_v [NS,HKV,DV] (NS <= 128)."""
+    optional attention sinks sink_k [NS,HKV,DQK], sink_v [NS,HKV,DV] (NS <= 128), or the
+    sequence's first n_first tokens (<= 128) staying visible."""
     _dev(q, k, v, gate, out, sink_k, sink_v)
+    if n_first and sink_k is not None:
+        raise ValueError("sink_k / sink_v and n_first are alternatives")
     B, S, H, DQK = q.shape
     T, HKV, DV = k.shape[1], k.shape[2], v.shape[-1]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
         out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
-    if sink_k is None:
+    if n_first:
+        _check(lib().dsa_window_attn_first(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
+                                           int(n_first), _ptr(gate), gm, float(sm_scale),
+                                           int(window), B, S, T, H, HKV, DQK, DV,
+                                           ATTN_ALGO[algo], _ptr(out), _stream(stream)))
+    elif sink_k is None:
         _check(lib().dsa_window_attn(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), gm,
                                      float(sm_scale), int(window), B, S, T, H, HKV, DQK, DV,
                                      ATTN_ALGO[algo], _ptr(out), _stream(stream)))
@@ -437,3 +470,169 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
                                            T, H, HKV, DQK, DV, ATTN_ALGO[algo], _ptr(out),
                                            _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------- paged cache
+def dsa_cache_row_bytes(fmt, kv_heads, dqk, dv) -> int:
+    """Bytes of one token's row; fmt "bf16" or "e2m1" (4 bits)."""
+    return int(lib().dsa_cache_row_bytes(CACHE_FORMAT[fmt], kv_heads, dqk, dv))
+
+
+def dsa_cache_pages(fmt, n_pages, page_size, kv_heads, dqk, dv, device="cuda"):
+    """Zeroed pages [n_pages, page_size, row]: bf16, or uint8 for the 4-bit format."""
+    row = dsa_cache_row_bytes(fmt, kv_heads, dqk, dv)
+    if row == 0:
+        raise ValueError(f"no cache row for {fmt} kv_heads={kv_heads} dqk={dqk} dv={dv}")
+    if fmt == "bf16":
+        return torch.zeros((n_pages, page_size, row // 2), dtype=torch.bfloat16, device=device)
+    return torch.zeros((n_pages, page_size, row), dtype=torch.uint8, device=device)
+
+
+class Cache:
+    """A paged key/value cache (include/dsa.h, section 5): pages [n_pages, page_size, row] (bf16
+    rows, or uint8 rows held in 4 bits) and the page table [B, max_pages] int32.  Holds the
+    tensors; the page table may be filled in place as sequences grow."""
+
+    def __init__(self, pages, table, kv_heads, dqk, dv, k_scale=1.0, v_scale=1.0):
+        _dev(pages, table)
+        fmt = {torch.bfloat16: "bf16", torch.uint8: "e2m1"}.get(pages.dtype)
+        if fmt is None:
+            raise ValueError("pages are bf16, or uint8 for the 4-bit format")
+        if table.dtype != torch.int32 or table.dim() != 2:
+            raise ValueError("table is int32 [B, max_pages]")
+        row = dsa_cache_row_bytes(fmt, kv_heads, dqk, dv)
+        if pages.dim() != 3 or row == 0 or pages.shape[2] * pages.element_size() != row:
+            raise ValueError(f"pages are [n_pages, page_size, row] with rows of {row} bytes for "
+                             f"{fmt} kv_heads={kv_heads} dqk={dqk} dv={dv}")
+        if table.device != pages.device:
+            raise ValueError("pages and table are on different devices")
+        self.pages, self.table = pages, table
+        self.kv_heads, self.dqk, self.dv = int(kv_heads), int(dqk), int(dv)
+        self.args = CacheArgs(format=CACHE_FORMAT[fmt], n_pages=pages.shape[0],
+                              page_size=pages.shape[1], max_pages=table.shape[1],
+                              HKV=self.kv_heads, DQK=self.dqk, DV=self.dv,
+                              k_scale=float(k_scale), v_scale=float(v_scale),
+                              pages=pages.data_ptr(), table=table.data_ptr())
+
+
+def _cache_check(cache, pos, shapes, types):
+    """The tensors of a cache call: contiguous, on the cache's device, which is the current one, of
+    the shapes and types named (None: not given).  Returns (B, S)."""
+    if pos.dim() != 2 or pos.shape[0] != cache.table.shape[0]:
+        raise ValueError(f"pos is [B, S] with B = {cache.table.shape[0]} (the table's rows)")
+    dev = cache.pages.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    for name, (t, shape) in shapes.items():
+        if t is None:
+            continue
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != types.get(name, torch.bfloat16):
+            raise ValueError(f"{name} has dtype {t.dtype}")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: libdsa takes contiguous CUDA tensors on the cache's device")
+
+
+def _cache_workspace(nbytes, device, ws, stream):
+    """The caller's workspace, or one of this call that its stream keeps until it is done."""
+    if nbytes == 0:
+        return None
+    if ws is not None:
+        _dev(ws)
+        if ws.numel() * ws.element_size() < nbytes:
+            raise ValueError(f"the workspace has fewer than {nbytes} bytes")
+        return ws
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=None, k_out=None,
+                     stream=None):
+    """Appends the tokens k [B,S,HKV,DQK], v [B,S,HKV,DV] at pos [B,S] (int32; negative: padding) to
+    the cache, the last 2*len(inv_freq) dims of each key head rotated by pos * inv_freq (rope
+    "interleaved": pairs (2j, 2j+1), or "half": pairs (j, j + len)), and rotates the same tokens'
+    queries q [B,S,H,DQK] into q_out (may be q).  k_out, if given, receives the rotated keys (may be
+    k).  Returns (rotated queries or None, k_out); with rope "off" q comes back as it is."""
+    B, S = pos.shape
+    KH = cache.kv_heads
+    H = KH if q is None else q.shape[2]
+    rotated = rope != "off"
+    if not rotated and q_out is not None:
+        raise ValueError("q_out goes with a rotation")
+    qs = (B, S, H, cache.dqk)
+    f = inv_freq if rotated else None
+    if rotated and f is None:
+        raise ValueError("a rotation needs inv_freq")
+    _cache_check(cache, pos, {
+        "pos": (pos, (B, S)), "k": (k, (B, S, KH, cache.dqk)), "v": (v, (B, S, KH, cache.dv)),
+        "q": (q, qs), "q_out": (q_out, qs), "k_out": (k_out, (B, S, KH, cache.dqk)),
+        "inv_freq": (f, (0 if f is None else f.numel(),))},
+        {"pos": torch.int32, "inv_freq": torch.float32})
+    if rotated and q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    _check(lib().dsa_cache_append(
+        ctypes.byref(cache.args), _ptr(pos), _ptr(k), _ptr(v), ROPE[rope],
+        2 * f.numel() if rotated else 0, _ptr(f), B, S, H, _ptr(q) if rotated else None,
+        _ptr(q_out), _ptr(k_out), _stream(stream)))
+    return (q_out if rotated else q), k_out
+
+
+def dsa_cache_read(cache, pos, k=None, v=None, stream=None):
+    """The tokens at pos [B,S] as the cache holds them: (k [B,S,HKV,DQK], v [B,S,HKV,DV]) in bf16,
+    zeros where it has no row."""
+    B, S = pos.shape
+    ks, vs = (B, S, cache.kv_heads, cache.dqk), (B, S, cache.kv_heads, cache.dv)
+    if k is None:
+        k = torch.empty(ks, dtype=torch.bfloat16, device=cache.pages.device)
+    if v is None:
+        v = torch.empty(vs, dtype=torch.bfloat16, device=cache.pages.device)
+    _cache_check(cache, pos, {"pos": (pos, (B, S)), "k": (k, ks), "v": (v, vs)},
+                 {"pos": torch.int32})
+    _check(lib().dsa_cache_read(ctypes.byref(cache.args), _ptr(pos), B, S, _ptr(k), _ptr(v),
+                                _stream(stream)))
+    return k, v
+
+
+def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, out, ws, stream):
+    B, S = pos.shape
+    H = q.shape[2]
+    gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
+    os_ = (B, S, H, cache.dv)
+    if out is None:
+        out = torch.empty(os_, dtype=torch.bfloat16, device=cache.pages.device)
+    K = 0 if idx is None else idx.shape[-1]
+    _cache_check(cache, pos, {
+        "pos": (pos, (B, S)), "q": (q, (B, S, H, cache.dqk)), "gate": (gate, (B, S, H)),
+        "out": (out, os_), "idx": (idx, (B, S, K))}, {"pos": torch.int32, "idx": torch.int32})
+    L, c = lib(), ctypes.byref(cache.args)
+    if idx is None:
+        nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, int(window), int(n_first)))
+        ws = _cache_workspace(nbytes, out.device, ws, stream)
+        _check(L.dsa_cache_attn(c, _ptr(q), _ptr(pos), int(window), int(n_first), _ptr(gate), gm,
+                                float(sm_scale), B, S, H, _ptr(out), _ptr(ws), nbytes,
+                                _stream(stream)))
+    else:
+        nbytes = int(L.dsa_cache_sparse_attn_workspace_bytes(c, B, S, H, K))
+        ws = _cache_workspace(nbytes, out.device, ws, stream)
+        _check(L.dsa_cache_sparse_attn(c, _ptr(q), _ptr(pos), _ptr(idx), K, _ptr(gate), gm,
+                                       float(sm_scale), B, S, H, _ptr(out), _ptr(ws), nbytes,
+                                       _stream(stream)))
+    return out
+
+
+def dsa_cache_attn(q, cache, pos, window=0, n_first=0, gate=None, gate_mode=None, sm_scale=0.0,
+                   out=None, ws=None, stream=None):
+    """Attention of the tokens q [B,S,H,DQK] at pos [B,S] over the cache: every key t <= pos
+    (window 0), or t > pos - window together with t < n_first."""
+    return _cache_attn(q, cache, pos, None, window, n_first, gate, gate_mode, sm_scale, out, ws,
+                       stream)
+
+
+def dsa_cache_sparse_attn(q, cache, pos, idx, gate=None, gate_mode=None, sm_scale=0.0, out=None,
+                          ws=None, stream=None):
+    """Attention of the tokens q [B,S,H,DQK] at pos [B,S] over the selected keys idx [B,S,K] of the
+    cache (int32, -1 padded, as dsa_topk and dsa_index_topk give them)."""
+    return _cache_attn(q, cache, pos, idx, 0, 0, gate, gate_mode, sm_scale, out, ws, stream)

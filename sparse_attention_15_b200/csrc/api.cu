@@ -606,13 +606,16 @@ dsa_status dsa_sparse_attn_latent(dsa_dtype dtype, const void* q, const void* kv
 
 static dsa_status window_attn_impl(dsa_dtype dtype, const void* q, const void* k, const void* v,
                                    const void* sink_k, const void* sink_v, int nsink,
-                                   const void* gate, dsa_gate_mode gate_mode, float sm_scale,
-                                   int window, int B, int S, int T, int H, int HKV, int DQK,
-                                   int DV, dsa_attn_algo algo, void* out, dsa_stream_t stream) {
+                                   int n_first, const void* gate, dsa_gate_mode gate_mode,
+                                   float sm_scale, int window, int B, int S, int T, int H,
+                                   int HKV, int DQK, int DV, dsa_attn_algo algo, void* out,
+                                   dsa_stream_t stream) {
   dsa_status st = dsa::check_attn_common(dtype, q, k, v, gate, gate_mode, sm_scale, B, S, T, H, HKV,
                                     DQK, DV, out);
   if (st != DSA_OK) return st;
   REQUIRE(window > 0, DSA_ERR_INVALID_ARG, "window must be positive");
+  REQUIRE(n_first >= 0, DSA_ERR_INVALID_ARG, "n_first must not be negative");
+  REQUIRE(n_first <= 128, DSA_ERR_UNSUPPORTED, "n_first=%d > 128", n_first);
   if ((st = check_sinks(sink_k, sink_v, nsink)) != DSA_OK) return st;
   REQUIRE(algo >= DSA_ATTN_AUTO && algo <= DSA_ATTN_MASKED_TILE, DSA_ERR_INVALID_ARG,
           "unknown attention algorithm %d", (int)algo);
@@ -624,8 +627,10 @@ static dsa_status window_attn_impl(dsa_dtype dtype, const void* q, const void* k
   p.gate = gate; p.gate_mode = (int)gate_mode; p.sm_scale = default_scale(sm_scale, DQK);
   p.B = B; p.S = S; p.T = T; p.H = H; p.HKV = HKV; p.DQK = DQK; p.DV = DV; p.q_off = T - S;
   p.out = out;
+  if (window > T) p.window = T;  // the same band; bounds the gather's key list
   p.sink_k = nsink > 0 ? sink_k : nullptr; p.sink_v = nsink > 0 ? sink_v : nullptr;
   p.nsink = nsink;
+  p.n_first = n_first;
   cudaStream_t s = (cudaStream_t)stream;
   // the band is dense work for every query block with at least a few rows: tensor cores
   if (algo == DSA_ATTN_MASKED_TILE || (algo == DSA_ATTN_AUTO && tc && S >= 64))
@@ -637,8 +642,17 @@ dsa_status dsa_window_attn(dsa_dtype dtype, const void* q, const void* k, const 
                            const void* gate, dsa_gate_mode gate_mode, float sm_scale,
                            int window, int B, int S, int T, int H, int HKV, int DQK, int DV,
                            dsa_attn_algo algo, void* out, dsa_stream_t stream) {
-  return window_attn_impl(dtype, q, k, v, nullptr, nullptr, 0, gate, gate_mode, sm_scale, window,
-                          B, S, T, H, HKV, DQK, DV, algo, out, stream);
+  return window_attn_impl(dtype, q, k, v, nullptr, nullptr, 0, 0, gate, gate_mode, sm_scale,
+                          window, B, S, T, H, HKV, DQK, DV, algo, out, stream);
+}
+
+dsa_status dsa_window_attn_first(dsa_dtype dtype, const void* q, const void* k, const void* v,
+                                 int n_first, const void* gate, dsa_gate_mode gate_mode,
+                                 float sm_scale, int window, int B, int S, int T, int H, int HKV,
+                                 int DQK, int DV, dsa_attn_algo algo, void* out,
+                                 dsa_stream_t stream) {
+  return window_attn_impl(dtype, q, k, v, nullptr, nullptr, 0, n_first, gate, gate_mode, sm_scale,
+                          window, B, S, T, H, HKV, DQK, DV, algo, out, stream);
 }
 
 dsa_status dsa_window_attn_sinks(dsa_dtype dtype, const void* q, const void* k, const void* v,
@@ -647,7 +661,7 @@ dsa_status dsa_window_attn_sinks(dsa_dtype dtype, const void* q, const void* k, 
                                  int window, int B, int S, int T, int H, int HKV, int DQK,
                                  int DV, dsa_attn_algo algo, void* out, dsa_stream_t stream) {
   REQUIRE(nsink > 0, DSA_ERR_INVALID_ARG, "nsink must be positive (use dsa_window_attn)");
-  return window_attn_impl(dtype, q, k, v, sink_k, sink_v, nsink, gate, gate_mode, sm_scale,
+  return window_attn_impl(dtype, q, k, v, sink_k, sink_v, nsink, 0, gate, gate_mode, sm_scale,
                           window, B, S, T, H, HKV, DQK, DV, algo, out, stream);
 }
 

@@ -9,7 +9,9 @@
 // applies the per-query selection bits (one bit per key, written by the top-k kernel), runs
 // an online softmax in float32 and accumulates O += P V on the tensor cores.  [SPARK]
 // "前向流程": out *= act(gate[b,s,h]) in float32 before the cast.  [PANGU] §3.2: the SWA
-// layers use the same core with the band s+q_off-W < t <= s+q_off and grouped KV heads.
+// layers use the same core with the band s+q_off-W < t <= s+q_off and grouped KV heads; where
+// the first tokens of the sequence stay visible (t < n_first <= 128), an item whose band starts
+// past key block 0 visits that block too, ahead of the band's.
 //
 // Layout of one work item: Q block [128 x Dqk], K block [128 x Dqk] (both K-major bf16,
 // 128-byte swizzle, via 3-D tensor maps over (dim, head, token)), V block [128 x Dv]
@@ -71,6 +73,7 @@ struct AttnArgs {
   int mask_stride;       // words per mask row (multiple of 4)
   int nqb;
   int nsink;             // attention sinks (PAS), 0..128: one extra block per item
+  int n_first;           // band: first tokens that stay visible, 0..128 (all in key block 0)
   // the key blocks each 128-query block visits (mask mode; NULL: every causal block):
   // bcount[b*nqb+qb] of them, in ascending order in blist[(b*nqb+qb)*nkb ...]
   const int* bcount;
@@ -185,20 +188,24 @@ __device__ __forceinline__ int sink_blocks(const AttnArgs& a) {
 struct KeyBlocks {
   const uint16_t* list;  // the item's key blocks, or NULL: every block of [j0, j1)
   int n, j0;
-  __device__ __forceinline__ int at(int r) const { return list ? (int)__ldg(list + r) : j0 + r; }
+  int lead;              // 1: key block 0 comes first (first tokens before a later band)
+  __device__ __forceinline__ int at(int r) const {
+    return list ? (int)__ldg(list + r) : (r < lead ? 0 : j0 + r - lead);
+  }
 };
 
 __device__ __forceinline__ KeyBlocks key_blocks(const AttnArgs& a, const Item& it, int j0,
                                                 int j1) {
   KeyBlocks kb;
   kb.j0 = j0;
+  kb.lead = a.n_first > 0 && j0 > 0 ? 1 : 0;
   if (a.blist) {
     const size_t q = (size_t)it.b * a.nqb + it.qb;
     kb.list = a.blist + q * a.nkb;
     kb.n = __ldg(a.bcount + q);
   } else {
     kb.list = nullptr;
-    kb.n = j1 - j0;
+    kb.n = j1 - j0 + kb.lead;
   }
   return kb;
 }
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       float m_used = ninf, l = 0.f;
       for (int j = 0; j < nb; ++j) {
         const uint32_t gg = g + j;
-        const int t0 = (j0 + j - sb) * kBlk + 64 * half;  // this half's first key
+        const int t0 = (j < sb ? 0 : kb.at(j - sb)) * kBlk + 64 * half;  // this half's first key
         uint32_t bits[2] = {0u, 0u};
         if (j < sb) {  // the sink block: its first nsink entries, visible to every query
 #pragma unroll
@@ -446,12 +453,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         } else if (row_ok) {
           // band: spos - window < t <= spos, t < T
           const int lo = max(spos - a.window + 1, 0) - t0, hi = min(spos, a.T - 1) - t0;
+          // first tokens: t < n_first, t <= spos (key block 0 alone)
+          const int first = min(a.n_first - 1, hi + t0) - t0;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int a0 = max(lo - 32 * w, 0), a1 = min(hi - 32 * w, 31);
             bits[w] = a1 < a0 ? 0u
                               : ((a1 - a0 == 31) ? 0xffffffffu
                                                  : (((1u << (a1 - a0 + 1)) - 1u) << a0));
+            const int f1 = first - 32 * w;
+            if (f1 >= 0) bits[w] |= f1 >= 31 ? 0xffffffffu : (2u << f1) - 1u;
           }
         }
         if (!warp_wait(&s_full[gg & 1], (gg >> 1) & 1)) { ok = false; break; }
@@ -1060,6 +1071,8 @@ cudaError_t launch_fa(const AttnProblem& p, const uint32_t* mask, int mask_strid
   a.B = p.B; a.S = p.S; a.T = p.T; a.H = p.H; a.HKV = p.HKV; a.q_off = p.q_off;
   a.window = p.window; a.mask_stride = mask_stride;
   a.nsink = sinks ? p.nsink : 0;
+  a.n_first = C::BAND ? p.n_first : 0;
+  if (a.n_first > kBlk) return cudaErrorNotSupported;  // one extra key block per item
   a.nqb = (p.S + kBlk - 1) / kBlk;
   a.bcount = bcount;
   a.blist = blist;

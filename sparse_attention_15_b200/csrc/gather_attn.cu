@@ -15,7 +15,8 @@
 // a slot by arriving on its "empty" barrier.
 //
 // The same kernel computes the sliding-window layers: the index set is then the band
-// s+q_off-window < t <= s+q_off, and query head h reads KV head h / (H / HKV).
+// s+q_off-window < t <= s+q_off, with the sequence's first tokens ahead of it where they stay
+// visible, and query head h reads KV head h / (H / HKV).
 //
 // Long index lists with few query rows (decode) are split over several CTAs; each writes
 // an unnormalised partial (o, m, l) and a second kernel merges them in a fixed order.
@@ -93,6 +94,7 @@ struct GatherArgs {
   const void* sink_k;       // [nsink, HKV, DQK] attention sinks (PAS) or NULL
   const void* sink_v;       // [nsink, HKV, DV]
   int nsink;
+  int n_first;              // band: first tokens that stay visible, listed before the band
   int skip_first_copy;      // testing aid: CTA 0 fills no slot
 };
 
@@ -103,7 +105,9 @@ __device__ __forceinline__ int key_at(const GatherArgs& a, const int32_t* idx_ro
                                       int spos) {
   if (SINKS && jj < a.nsink) return -2 - jj;
   const int e = SINKS ? jj - a.nsink : jj;
-  const int t = idx_row ? __ldg(idx_row + e) : spos - a.window + 1 + e;  // band: oldest first
+  if (!idx_row && e < a.n_first) return e <= spos - a.window ? e : -1;  // not in the band too
+  // band: oldest first
+  const int t = idx_row ? __ldg(idx_row + e) : spos - a.window + 1 + (e - a.n_first);
   return (t >= 0 && t < a.T && t <= spos) ? t : -1;
 }
 
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(544, HPW <= 2 ? 2 : 1) gather_attn_kernel(cons
   const int split = blockIdx.x % a.nsplit;
   const int b = row / a.S, s = row % a.S;
   const int spos = s + a.q_off;
-  const int nkeys_total = (SINKS ? a.nsink : 0) + (a.idx ? a.K : a.window);
+  const int nkeys_total = (SINKS ? a.nsink : 0) + (a.idx ? a.K : a.n_first + a.window);
   const int j0 = split * a.keys_per_split;
   const int nkeys = max(0, min(nkeys_total, j0 + a.keys_per_split) - j0);
   const int32_t* idx_row = a.idx ? a.idx + (size_t)row * a.K : nullptr;
@@ -477,7 +481,8 @@ cudaError_t launch_gather_attn(const AttnProblem& p, void* ws, size_t ws_bytes,
   if (rows == 0) return cudaSuccess;
   a.sink_k = p.sink_k; a.sink_v = p.sink_v; a.nsink = p.sink_k ? p.nsink : 0;
   a.skip_first_copy = g_arm_skip_copy.exchange(0);
-  const int nkeys = a.nsink + (p.idx ? p.K : p.window);
+  a.n_first = p.idx ? 0 : p.n_first;
+  const int nkeys = a.nsink + (p.idx ? p.K : p.n_first + p.window);
   split_policy(rows, nkeys, &a.nsplit, &a.keys_per_split, p.idx != nullptr);
   a.key_list_bytes = ((uint32_t)a.keys_per_split * 4u + 127u) & ~127u;
   if (a.nsplit > 1) {

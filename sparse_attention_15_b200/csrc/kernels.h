@@ -117,6 +117,7 @@ struct AttnProblem {
   const void* sink_k = nullptr;  // [nsink,HKV,DQK] attention sinks (PAS), or NULL
   const void* sink_v = nullptr;  // [nsink,HKV,DV]
   int nsink = 0;
+  int n_first = 0;  // band: the sequence's first tokens that stay visible
 };
 size_t gather_attn_workspace_bytes(int B, int S, int H, int DV, int K, int nsink = 0);
 // Testing aid: the next launch_gather_attn makes its first CTA fill none of its key slots,
@@ -155,6 +156,41 @@ struct LatentProblem {
   int B, S, T, H, DQK, DV, q_off;
   void* out;           // [B,S,H,DV]
 };
+// The paged key/value cache (cache.cuh): append with rotation, reading back, attention.
+struct CacheView;
+struct CacheAppendProblem {
+  const CacheView& cache;
+  const void* q;        // [B,S,H,DQK] bf16 or NULL
+  const void* k;        // [B,S,HKV,DQK] bf16
+  const void* v;        // [B,S,HKV,DV] bf16
+  const int32_t* pos;   // [B,S]
+  int rope_mode;        // 0 off, 1 interleaved pairs, 2 half-split pairs
+  int rope_dim;         // the rotated last dims
+  const float* inv_freq;  // [rope_dim / 2]
+  int B, S, H;
+  void* q_out;
+  void* k_out;          // or NULL
+};
+cudaError_t launch_cache_append(const CacheAppendProblem& p, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheView& c, const int32_t* pos, int B, int S, void* k,
+                              void* v, cudaStream_t st);
+struct CacheAttnProblem {
+  const CacheView& cache;
+  const void* q;        // [B,S,H,DQK] bf16
+  const int32_t* pos;   // [B,S]
+  const int32_t* idx;   // [B,S,K], or NULL for the window form
+  int K, window, n_first;  // window 0: every key t <= pos
+  const void* gate;     // [B,S,H] bf16 or NULL
+  int gate_mode;
+  float sm_scale;
+  int B, S, H;
+  void* out;            // [B,S,H,DV] bf16
+};
+bool cache_attn_supported(int format, int H, int HKV, int DQK, int DV);
+size_t cache_attn_workspace_bytes(const CacheAttnProblem& p);
+cudaError_t launch_cache_attn(const CacheAttnProblem& p, void* ws, size_t ws_bytes,
+                              cudaStream_t st);
+
 bool latent_attn_supported(int dtype, int H, int DQK, int DV);
 size_t latent_attn_workspace_bytes(int B, int S, int H, int K, int nsink);
 cudaError_t launch_latent_attn(const LatentProblem& p, void* ws, size_t ws_bytes,

@@ -289,3 +289,137 @@ def test_binding_fails_loudly_without_library(monkeypatch):
     monkeypatch.setattr(dsa, "LIB_PATH", "/nonexistent/libdsa.so")
     with pytest.raises(RuntimeError, match="no fallback"):
         dsa.lib()
+
+
+# ----------------------------------------------------------------------------- the paged cache
+def _cache_args(dsa, **kw):
+    a = dict(format=1, n_pages=4, page_size=16, max_pages=8, HKV=8, DQK=192, DV=128, k_scale=1.0,
+             v_scale=1.0, pages=0x10000, table=0x10000)
+    a.update(kw)
+    return dsa.CacheArgs(**a)
+
+
+CACHE_FAULTS = [  # field changes, status
+    (dict(format=2), 1), (dict(format=-1), 1), (dict(n_pages=0), 1), (dict(page_size=0), 1),
+    (dict(max_pages=-1), 1), (dict(HKV=0), 1), (dict(DQK=96), 2), (dict(DQK=256), 2),
+    (dict(DV=192), 2), (dict(HKV=65), 2), (dict(max_pages=1 << 20, page_size=1025), 2),
+    (dict(pages=None), 1), (dict(table=None), 1), (dict(k_scale=0.0), 1),
+    (dict(k_scale=float("nan")), 1), (dict(v_scale=float("inf")), 1), (dict(v_scale=-1.0), 1),
+    (dict(format=0, k_scale=2.0), 1), (dict(format=0, v_scale=0.5), 1), (dict(pages=0x10008), 2),
+    (dict(table=0x10002), 2)]
+
+
+def test_cache_calls_reject_a_bad_cache(lib):
+    L, ref = lib.lib(), ctypes.byref
+    for change, status in CACHE_FAULTS:
+        c = _cache_args(lib, **change)
+        assert L.dsa_cache_append(ref(c), FAKE, FAKE, FAKE, 0, 0, None, 1, 1, 8, None, None, None,
+                                  None) == status, change
+        assert L.dsa_cache_read(ref(c), FAKE, 1, 1, FAKE, FAKE, None) == status, change
+        assert L.dsa_cache_attn(ref(c), FAKE, FAKE, 0, 0, None, 0, 0.0, 1, 1, 8, FAKE, FAKE,
+                                1 << 40, None) == status, change
+        assert L.dsa_cache_sparse_attn(ref(c), FAKE, FAKE, FAKE, 4, None, 0, 0.0, 1, 1, 8, FAKE,
+                                       FAKE, 1 << 40, None) == status, change
+    for call in (lambda: L.dsa_cache_read(None, FAKE, 1, 1, FAKE, FAKE, None),
+                 lambda: L.dsa_cache_read(ref(_cache_args(lib)), FAKE, 0, 1, FAKE, FAKE, None),
+                 lambda: L.dsa_cache_read(ref(_cache_args(lib)), FAKE, 1, -1, FAKE, FAKE, None),
+                 lambda: L.dsa_cache_read(ref(_cache_args(lib)), None, 1, 1, FAKE, FAKE, None),
+                 lambda: L.dsa_cache_read(ref(_cache_args(lib)), FAKE, 1, 1, None, FAKE, None)):
+        assert call() == 1
+    assert L.dsa_cache_read(ref(_cache_args(lib)), FAKE, 1, 1, FAKE_MIS, FAKE, None) == 2
+    assert L.dsa_cache_read(ref(_cache_args(lib)), FAKE, 1 << 13, 1 << 12, FAKE, FAKE, None) == 2
+
+
+def test_cache_row_bytes(lib):
+    row = lib.dsa_cache_row_bytes
+    assert row("bf16", 8, 192, 128) == 8 * 320 * 2
+    assert row("e2m1", 8, 192, 128) == 8 * 320 * 9 // 16
+    assert row("e2m1", 1, 64, 64) == 80      # 72 and padding
+    assert row("e2m1", 1, 100, 64) == 0 and row("bf16", 0, 64, 64) == 0
+    assert lib.lib().dsa_cache_row_bytes(7, 1, 64, 64) == 0
+
+
+def test_cache_append_rejects_bad_arguments(lib):
+    L = lib.lib()
+
+    def call(**kw):
+        a = dict(k=FAKE, v=FAKE, mode=1, dim=64, inv=FAKE, H=32, q=FAKE, q_out=FAKE, k_out=None)
+        a.update(kw)
+        return L.dsa_cache_append(ctypes.byref(_cache_args(lib)), FAKE, a["k"], a["v"], a["mode"],
+                                  a["dim"], a["inv"], 1, 1, a["H"], a["q"], a["q_out"],
+                                  a["k_out"], None)
+
+    assert call(k=None) == 1 and call(v=None) == 1
+    assert call(mode=3) == 1 and call(mode=-1) == 1
+    assert call(dim=0) == 1 and call(inv=None) == 1
+    assert call(dim=48) == 2 and call(dim=224) == 2
+    assert call(inv=ctypes.c_void_p(0x10001)) == 2
+    assert call(q=None) == 1 and call(q_out=None) == 1
+    assert call(H=0) == 1 and call(H=12) == 1 and call(H=72) == 2
+    assert call(mode=0) == 1                                    # q without a rotation
+    assert call(mode=0, dim=0, inv=None, q=None) == 1           # q_out without one
+    assert call(k=FAKE_MIS) == 2 and call(q_out=FAKE_MIS) == 2 and call(k_out=FAKE_MIS) == 2
+
+
+def test_cache_attn_rejects_bad_arguments(lib):
+    L = lib.lib()
+
+    def call(fn="dsa_cache_attn", cache=None, **kw):
+        a = dict(q=FAKE, a=64, b=4, gate=None, gm=0, sm=0.0, H=32, out=FAKE, ws=FAKE, wsb=1 << 40)
+        a.update(kw)
+        c = cache or _cache_args(lib, max_pages=1 << 16)
+        mid = [a["a"], a["b"]]
+        return getattr(L, fn)(ctypes.byref(c), a["q"], FAKE, *mid, a["gate"], a["gm"], a["sm"], 1,
+                              1, a["H"], a["out"], a["ws"], a["wsb"], None)
+
+    assert call(a=-1) == 1 and call(b=-1) == 1
+    assert call(a=0, b=4) == 1                    # first tokens without a window
+    assert call(q=None) == 1 and call(out=None) == 1
+    assert call(gm=3, gate=FAKE) == 1 and call(gm=1) == 1 and call(gate=FAKE) == 1
+    assert call(sm=float("nan")) == 1 and call(sm=float("inf")) == 1
+    assert call(H=12) == 1 and call(H=0) == 1 and call(H=128) == 2
+    assert call(q=FAKE_MIS) == 2 and call(out=FAKE_MIS) == 2
+    assert call(gm=1, gate=FAKE_MIS) == 2
+    need = L.dsa_cache_attn_workspace_bytes(ctypes.byref(_cache_args(lib, max_pages=1 << 16)), 1, 1,
+                                            32, 0, 0)
+    assert need > 0
+    assert call(a=0, b=0, ws=None) == 1 and call(a=0, b=0, wsb=need - 1) == 1
+    assert b"workspace" in L.dsa_last_error()
+    assert call(a=0, b=0, ws=FAKE_MIS) == 2
+    s = "dsa_cache_sparse_attn"
+    assert call(s, a=None, b=8) == 1 and call(s, a=FAKE, b=0) == 1
+    assert call(s, a=FAKE_MIS, b=8) == 2 and call(s, a=FAKE, b=(1 << 30) + 1) == 2
+    # 4-bit parts of a row must be whole 16-byte pieces above 16 KV heads
+    assert call(cache=_cache_args(lib, HKV=18), H=18) == 2
+    for bad in (dict(format=9), dict(DQK=100), dict(HKV=0)):
+        c = ctypes.byref(_cache_args(lib, **bad))
+        assert L.dsa_cache_attn_workspace_bytes(c, 1, 1, 32, 0, 0) == 0
+        assert L.dsa_cache_sparse_attn_workspace_bytes(c, 1, 1, 32, 64) == 0
+    assert L.dsa_cache_attn_workspace_bytes(None, 1, 1, 32, 0, 0) == 0
+
+
+def test_window_attn_first_rejects_bad_arguments(lib):
+    L = lib.lib()
+
+    def call(n_first, window=8):
+        return L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, n_first, None, 0, 0.0, window, 1, 64, 64,
+                                       4, 2, 128, 128, 0, None, None)
+
+    assert L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, -1, None, 0, 0.0, 8, 1, 64, 64, 4, 2, 128,
+                                   128, 0, FAKE, None) == 1
+    assert L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, 129, None, 0, 0.0, 8, 1, 64, 64, 4, 2, 128,
+                                   128, 0, FAKE, None) == 2
+    assert call(4) == 1  # no output
+
+
+def test_binding_checks_of_the_cache(lib):
+    import torch
+
+    with pytest.raises(ValueError):
+        lib.dsa_cache_pages("e2m1", 4, 16, 8, 100, 128, device="cpu")
+    pages = lib.dsa_cache_pages("e2m1", 4, 16, 8, 192, 128, device="cpu")
+    assert pages.shape == (4, 16, 1440) and pages.dtype == torch.uint8
+    with pytest.raises(ValueError):  # not a CUDA tensor
+        lib.Cache(pages, torch.zeros(1, 4, dtype=torch.int32), 8, 192, 128)
+    with pytest.raises(ValueError):  # PAS sinks and first tokens
+        lib.dsa_window_attn(pages, pages, pages, 8, sink_k=pages, sink_v=pages, n_first=4)
