@@ -409,8 +409,8 @@ dsa_status dsa_window_attn_first(dsa_dtype dtype, const void* q, const void* k, 
  *          negative one marks padding.
  *   k_scale, v_scale  > 0, finite: the 4-bit form's scale of the whole tensor (a power of two
  *          keeps it exact); 1 with DSA_CACHE_BF16.
- *   DQK in {64, 128, 192}, DV in {64, 128}, HKV <= 64, max_pages * page_size <= 2^30; everything
- *   is bf16 outside the cache.
+ *   DQK in {64, 128, 192}, DV in {64, 128}, HKV <= 64, max_pages * page_size <= 2^30,
+ *   n_pages * page_size < 2^31; everything is bf16 outside the cache.
  * --------------------------------------------------------------------------------- */
 typedef enum { DSA_CACHE_BF16 = 0, DSA_CACHE_E2M1 = 1 } dsa_cache_format;
 /* Pairs of the rotated dims: (2j, 2j+1), or (j, j + rope_dim/2). */
@@ -461,8 +461,8 @@ dsa_status dsa_cache_read(const dsa_cache* cache, const int32_t* pos, int B, int
  *   gate, gate_mode, sm_scale (<= 0: 1/sqrt(DQK)), out [B,S,H,DV]: as dsa_sparse_attn.  Keys a
  *   query does not see are not read, whatever they hold.  A row without keys (padding, a context
  *   without pages) gets zeros.  Every visible key must have been appended.
- *   H <= 64; HKV a multiple of 4 above 16 with DSA_CACHE_E2M1.  Workspace (partial results of key
- *   slices) from dsa_cache_attn_workspace_bytes; 0 -> NULL is fine.
+ *   H <= 64.  Workspace (partial results of key slices) from dsa_cache_attn_workspace_bytes; 0 ->
+ *   NULL is fine.
  */
 size_t dsa_cache_attn_workspace_bytes(const dsa_cache* cache, int B, int S, int H, int window,
                                       int n_first);

@@ -58,7 +58,7 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
 // Two e4m3 values (low byte first) as an f16 pair; exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t v) {
   uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+  asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
       : "=r"(r)
       : "r"(v));
   return r;

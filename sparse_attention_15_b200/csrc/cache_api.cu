@@ -52,6 +52,8 @@ dsa_status check_shape(const dsa_cache* c, int B, int S) {
   REQUIRE(c->HKV <= 64, DSA_ERR_UNSUPPORTED, "HKV=%d > 64", c->HKV);
   REQUIRE((long long)c->max_pages * c->page_size <= (1LL << 30), DSA_ERR_UNSUPPORTED,
           "max_pages * page_size must be at most 2^30");
+  REQUIRE((long long)c->n_pages * c->page_size < (1LL << 31), DSA_ERR_UNSUPPORTED,
+          "n_pages * page_size must be below 2^31");
   REQUIRE((long long)B * S <= (1LL << 24), DSA_ERR_UNSUPPORTED, "B*S=%lld > 2^24",
           (long long)B * S);
   return DSA_OK;
@@ -116,7 +118,7 @@ dsa_status run_attn(const char* what, const dsa_cache* c, const void* q, const i
   REQUIRE(aligned16(q) && aligned16(out) && aligned16(gate), DSA_ERR_UNSUPPORTED,
           "pointers must be 16-byte aligned");
   REQUIRE(dsa::cache_attn_supported((int)c->format, H, c->HKV, c->DQK, c->DV), DSA_ERR_UNSUPPORTED,
-          "no kernel for H=%d HKV=%d (4-bit rows: HKV a multiple of 4 above 16)", H, c->HKV);
+          "no kernel for H=%d HKV=%d", H, c->HKV);
   const dsa::CacheView v = view(c);
   dsa::CacheAttnProblem p{v, q, pos, idx, K, window, n_first, gate, (int)gm,
                           sm_scale > 0.f ? sm_scale : 1.0f / sqrtf((float)c->DQK), B, S, H, out};

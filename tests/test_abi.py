@@ -389,8 +389,6 @@ def test_cache_attn_rejects_bad_arguments(lib):
     s = "dsa_cache_sparse_attn"
     assert call(s, a=None, b=8) == 1 and call(s, a=FAKE, b=0) == 1
     assert call(s, a=FAKE_MIS, b=8) == 2 and call(s, a=FAKE, b=(1 << 30) + 1) == 2
-    # 4-bit parts of a row must be whole 16-byte pieces above 16 KV heads
-    assert call(cache=_cache_args(lib, HKV=18), H=18) == 2
     for bad in (dict(format=9), dict(DQK=100), dict(HKV=0)):
         c = ctypes.byref(_cache_args(lib, **bad))
         assert L.dsa_cache_attn_workspace_bytes(c, 1, 1, 32, 0, 0) == 0
