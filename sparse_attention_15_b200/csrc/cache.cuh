@@ -17,8 +17,21 @@ struct CacheView {
   int HKV, DQK, DV;
   float k_scale, v_scale;
   long long row_bytes;
-  long long cap;         // max_pages * page_size: keys a sequence can hold
+  int cap;               // max_pages * page_size: keys a sequence can hold, at most 2^30
+  uint32_t page_mul;     // t / page_size = (t * page_mul) >> 32 >> page_shift for t < 2^31
+  int page_shift;        // (page_size 1: page_mul 0)
 };
+
+// The divisor's multiplier: ceil(2^(31 + L) / d) with L = ceil(log2 d), which fits 32 bits and
+// rounds every quotient of a 31-bit number down correctly.
+inline void set_page_divisor(CacheView* c) {
+  int L = 0;
+  while ((1LL << L) < c->page_size) ++L;
+  c->page_shift = L > 0 ? L - 1 : 0;
+  c->page_mul =
+      L > 0 ? (uint32_t)(((1ULL << (31 + L)) + c->page_size - 1) / (unsigned long long)c->page_size)
+            : 0;
+}
 
 // Byte offsets inside a row.  bf16: [K | V]; e2m1: [K codes | V codes | K scales | V scales],
 // two codes to a byte (even element low), one e4m3 scale for 16 elements of a head.
@@ -36,14 +49,14 @@ __host__ __device__ inline int cache_vs_off(int HKV, int DQK, int DV) {
   return HKV * (DQK + DV) / 2 + HKV * DQK / 16;
 }
 
-// The physical row (page * page_size + slot) of token t of sequence b, or -1 if the cache has none:
-// t out of range, or a table entry that names no page.
-__device__ __forceinline__ long long cache_row(const CacheView& c, int b, int t) {
-  if (t < 0 || (long long)t >= c.cap) return -1;
-  const int p = t / c.page_size;
-  const int page = __ldg(c.table + (size_t)b * c.max_pages + p);
-  if (page < 0 || page >= c.n_pages) return -1;
-  return (long long)page * c.page_size + (t - p * c.page_size);
+// The physical row (page * page_size + slot, below 2^31) of token t of a sequence with this table
+// row, or -1 if the cache has none: t out of range, or a table entry that names no page.
+__device__ __forceinline__ int cache_row(const CacheView& c, const int32_t* table_row, int t) {
+  if ((uint32_t)t >= (uint32_t)c.cap) return -1;
+  const int p = c.page_mul ? (int)(__umulhi((uint32_t)t, c.page_mul) >> c.page_shift) : t;
+  const int page = __ldg(table_row + p);
+  if ((uint32_t)page >= (uint32_t)c.n_pages) return -1;
+  return page * c.page_size + (t - p * c.page_size);
 }
 
 // Four e2m1 pairs (the bytes of w, low element first) as f16 pairs; exact.

@@ -82,7 +82,8 @@ dsa::CacheView view(const dsa_cache* c) {
   v.HKV = c->HKV; v.DQK = c->DQK; v.DV = c->DV;
   v.k_scale = c->k_scale; v.v_scale = c->v_scale;
   v.row_bytes = dsa::cache_row_bytes(v.format, v.HKV, v.DQK, v.DV);
-  v.cap = (long long)c->max_pages * c->page_size;
+  v.cap = c->max_pages * c->page_size;
+  dsa::set_page_divisor(&v);
   return v;
 }
 

@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
     int u = i - ti * per;
     const long long tok = tok0 + ti;
     const int p = __ldg(a.pos + tok);
-    const long long r = u < uq ? -1 : cache_row(c, (int)(tok / a.S), p);
+    const int b = (int)(tok / a.S);
+    const long long r = u < uq ? -1 : cache_row(c, c.table + (size_t)b * c.max_pages, p);
     uint8_t* row = r >= 0 ? c.pages + r * c.row_bytes : nullptr;
     if (u >= uq + uk) {  // a group of V
       u -= uq + uk;
@@ -247,7 +248,8 @@ __global__ void __launch_bounds__(kThreads)
        i += (long long)gridDim.x * kThreads) {
     const long long tok = i / per;
     const int u = (int)(i - tok * per);
-    const long long r = cache_row(c, (int)(tok / S), __ldg(pos + tok));
+    const int b = (int)(tok / S);
+    const long long r = cache_row(c, c.table + (size_t)b * c.max_pages, __ldg(pos + tok));
     const uint8_t* row = c.pages + (r >= 0 ? r : 0) * c.row_bytes;
     if (u < uk) {
       store_group(k + (size_t)tok * uk * 16 + u * 16,

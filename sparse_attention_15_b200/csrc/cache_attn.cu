@@ -74,7 +74,7 @@ __global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
     const KeyList l = key_list(a, row, pos);
     int j0, j1;
     key_slice(l, a.nsplit, split, &j0, &j1);
-    const int b = row / a.S;
+    const int32_t* table = a.c.table + (size_t)(row / a.S) * a.c.max_pages;
     const uint32_t bytes = (uint32_t)(kb + vb);
     int fills = 0;
     bool ok = true;
@@ -91,7 +91,7 @@ __global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
     };
     auto look_up = [&] {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = t[i] <= pos ? cache_row(a.c, b, t[i]) : -1;
+      for (int i = 0; i < 4; ++i) r[i] = t[i] <= pos ? cache_row(a.c, table, t[i]) : -1;
     };
     auto after = [&](int j) { return j1 - j > ks ? j + ks : j1; };
     read_keys(j0);

@@ -77,9 +77,9 @@ __device__ __forceinline__ KeyList key_list(const CacheAttnArgs& a, int row, int
   } else if (a.idx) {
     l.n = a.K;
   } else {
-    const int hi = (long long)pos < a.c.cap ? pos : (int)(a.c.cap - 1);  // cap <= 2^30
+    const int hi = min(pos, a.c.cap - 1);
     l.low = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-    l.nf = (int)min((long long)min(a.n_first, l.low), a.c.cap);
+    l.nf = min(min(a.n_first, l.low), a.c.cap);
     l.n = l.nf + max(0, hi - l.low + 1);
   }
   return l;

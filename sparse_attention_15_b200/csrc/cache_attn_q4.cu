@@ -62,6 +62,13 @@ __device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[1]) {
 __device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[2]) {
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
 }
+__device__ __forceinline__ void load_words4(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c,
+                                            uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(at)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t load_byte(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2) cache_attn_q4_kernel(const C
   const int split = blockIdx.x % a.nsplit;
   const int hg = (blockIdx.x / a.nsplit) % a.nhg;
   const int row = blockIdx.x / (a.nsplit * a.nhg);
-  const int b = row / a.S;
+  const int32_t* table = a.c.table + (size_t)(row / a.S) * a.c.max_pages;
   const int kv0 = hg * a.hc;
   const int kg = warp / nhw, hw = warp % nhw;
   const int kv = kv0 + hw / a.nsub, sub = hw % a.nsub;
@@ -103,11 +110,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2) cache_attn_q4_kernel(const C
   // l & 15 of step l >> 4 of a pair, reads it two pairs ahead and looks its row up one ahead.
   const int steps = (((j1 - j0 + 15) >> 4) - kg + a.kw - 1) / a.kw;
   const int my_j = j0 + 16 * (kg + a.kw * (lane >> 4)) + (lane & 15);
-  auto read_key = [&](int pair) {
-    const long long e = my_j + 32LL * a.kw * pair;
-    return e < j1 ? list.at((int)e) : -1;
+  auto read_key = [&](int pair) {  // (below j1 + 2^10: no overflow)
+    const int e = my_j + 32 * a.kw * pair;
+    return e < j1 ? list.at(e) : -1;
   };
-  auto look_up = [&](int t) { return t <= pos ? (int)cache_row(a.c, b, t) : -1; };
+  auto look_up = [&](int t) { return t <= pos ? cache_row(a.c, table, t) : -1; };
   int rn = look_up(read_key(0)), tn = read_key(1);
 
   // ---- copies: lane = piece `at` of key `at_key` (of KEYS) in row 0 and in the step's first slots
@@ -131,13 +138,21 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2) cache_attn_q4_kernel(const C
   const uint32_t row_bytes = (uint32_t)a.c.row_bytes;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * S::STEP);
   const uint32_t fill_at = ring + at_key * S::PITCH + 16 * at;
-  // the step whose rows are in lanes half * 16 .. of r; a key without a row reads row 0
-  auto fill = [&](uint32_t stage, int r, int half) {
+  // A pair's rows, as a thread needs them: its keys at_key, at_key + KEYS, ... of a step in a row of
+  // `rows` (key 0 of the pair in its word 0); a key without a row reads row 0.
+  uint32_t* rows = reinterpret_cast<uint32_t*>(smem + kQ4Warps * kStages * S::STEP) + 32 * warp;
+  const int my_word = (lane & 16) + (lane & (S::KEYS - 1)) * (16 / S::KEYS) + (lane & 15) / S::KEYS;
+  const uint32_t rows_at = smem_u32(rows) + at_key * (4 * 16 / S::KEYS);
+  auto fill = [&](uint32_t stage, int half) {
+    uint32_t rk[16 / S::KEYS];
 #pragma unroll
-    for (int i = 0; i < 16; i += S::KEYS) {
-      const uint32_t rk = (uint32_t)__shfl_sync(0xffffffffu, r, 16 * half + i + at_key);
-      if (has_piece)
-        cp_async16(fill_at + stage + i * S::PITCH, from + (unsigned long long)rk * row_bytes);
+    for (int i = 0; i < 16 / S::KEYS; i += 4)
+      load_words4(rows_at + 64 * half + 4 * i, rk[i], rk[i + 1], rk[i + 2], rk[i + 3]);
+    if (has_piece) {
+#pragma unroll
+      for (int i = 0; i < 16 / S::KEYS; ++i)
+        cp_async16(fill_at + stage + i * S::KEYS * S::PITCH,
+                   from + (unsigned long long)rk[i] * row_bytes);
     }
   };
 
@@ -194,102 +209,111 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2) cache_attn_q4_kernel(const C
   const uint32_t v_at0 = ring + k0 * S::PITCH + S::V + g * (VPT / 2);
   const uint32_t v_at1 = ring + k1 * S::PITCH + S::V + g * (VPT / 2);
   const uint32_t vs_off = S::VS - S::V + (vs0 & 15) + (g * VPT) / 16 - g * (VPT / 2);
+  // one step: the 16 keys in slots `base` .., of which `mask` have a row
+  auto step = [&](uint32_t base, uint32_t mask) {
+    // S^T = K Q^T, two accumulators
+    float s[2][4];
+    const uint32_t ra = k_at + base, rb = ra + 8 * S::PITCH;
+    const uint32_t rsa = ks_at + base, rsb = rsa + 8 * S::PITCH;
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+      uint32_t wa[2], wb[2];
+      load_words(ra + c * 32, wa);
+      load_words(rb + c * 32, wb);
+      const uint32_t sa = e4m3x2_to_f16(load_byte(rsa + c * 4) * 0x0101u);
+      const uint32_t sb = e4m3x2_to_f16(load_byte(rsb + c * 4) * 0x0101u);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t xa[4], xb[4];
+        e2m1x8_to_f16(wa[hf], xa);
+        e2m1x8_to_f16(wb[hf], xb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t f[4] = {mul_f16x2(xa[2 * i], sa), mul_f16x2(xb[2 * i], sb),
+                                 mul_f16x2(xa[2 * i + 1], sa), mul_f16x2(xb[2 * i + 1], sb)};
+          if (c == 0 && hf == 0)
+            mma_f16_zero(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
+          else
+            mma_f16(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
+        }
+      }
+    }
+    // this thread's values, on their way while the softmax runs
+    const uint32_t v0 = v_at0 + base, v1 = v_at1 + base, v2 = v0 + 8 * S::PITCH,
+                   v3 = v1 + 8 * S::PITCH;
+    uint32_t vw[4][VPT / 8];
+    load_words(v0, vw[0]);
+    load_words(v1, vw[1]);
+    load_words(v2, vw[2]);
+    load_words(v3, vw[3]);
+    uint32_t sc0 = load_byte(v0 + vs_off) | (load_byte(v1 + vs_off) << 8);
+    uint32_t sc1 = load_byte(v2 + vs_off) | (load_byte(v3 + vs_off) << 8);
+
+    float x[4] = {(s[0][0] + s[1][0]) * cs[0], (s[0][1] + s[1][1]) * cs[1],
+                  (s[0][2] + s[1][2]) * cs[0], (s[0][3] + s[1][3]) * cs[1]};
+    if (mask != 0xffffu) {  // row 0 stands in for a missing key: its scale may be NaN
+      if (!((mask >> ka) & 1u)) x[0] = x[1] = -INFINITY;
+      if (!((mask >> (ka + 8)) & 1u)) x[2] = x[3] = -INFINITY;
+      sc0 &= (((mask >> k0) & 1u) * 0xffu) | (((mask >> k1) & 1u) * 0xff00u);
+      sc1 &= (((mask >> (k0 + 8)) & 1u) * 0xffu) | (((mask >> (k1 + 8)) & 1u) * 0xff00u);
+    }
+    float p[4];
+    softmax_step<TOP, MT>(x, m, l, o, p);
+    const __half2 p01 = __floats2half2_rn(p[0], p[1]), p23 = __floats2half2_rn(p[2], p[3]);
+    const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p01));
+    const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p23));
+    const uint32_t s01 = e4m3x2_to_f16(sc0), s23 = e4m3x2_to_f16(sc1);
+    // O^T += V^T P^T
+#pragma unroll
+    for (int w = 0; w < VPT / 8; ++w) {
+      constexpr uint32_t kLo = 0x0f0f0f0fu;
+      uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, two keys each
+      e2m1x8_to_f16((vw[0][w] & kLo) | ((vw[1][w] << 4) & ~kLo), e01);
+      e2m1x8_to_f16(((vw[0][w] >> 4) & kLo) | (vw[1][w] & ~kLo), o01);
+      e2m1x8_to_f16((vw[2][w] & kLo) | ((vw[3][w] << 4) & ~kLo), e23);
+      e2m1x8_to_f16(((vw[2][w] >> 4) & kLo) | (vw[3][w] & ~kLo), o23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t f[4] = {mul_f16x2(e01[i], s01), mul_f16x2(o01[i], s01),
+                               mul_f16x2(e23[i], s23), mul_f16x2(o23[i], s23)};
+        mma_f16(o[4 * w + i], f, b0, b1);
+      }
+    }
+  };
+
   static_assert(kAhead == 2, "a pair of steps is copied while the pair before is worked on");
-  uint32_t masks = __ballot_sync(0xffffffffu, rn >= 0), masks_n = 0;  // keys with a row: of a pair
-  int r = max(rn, 0);
-  fill(0, r, 0);
-  cp_async_commit();
-  fill(S::STEP, r, 1);
-  cp_async_commit();
-  uint32_t base = 0, fill_base = 2 * S::STEP;
+  uint32_t masks, masks_n = __ballot_sync(0xffffffffu, rn >= 0);  // keys with a row, of a pair
+  rows[my_word] = max(rn, 0);
   rn = look_up(tn);
   tn = read_key(2);
-  for (int n = 0; n < steps; ++n) {
-    if ((n & 1) == 0) {  // the next pair's rows
-      masks_n = __ballot_sync(0xffffffffu, rn >= 0);
-      r = max(rn, 0);
-      rn = look_up(tn);
-      tn = read_key((n >> 1) + 3);
-    }
-    if (n + kAhead < steps) fill(fill_base, r, n & 1);
-    cp_async_commit();
-    cp_async_wait<kAhead>();  // this step's copies have landed
+  __syncwarp();
+  fill(0, 0);
+  cp_async_commit();
+  fill(S::STEP, 1);
+  cp_async_commit();
+  uint32_t at_step = 0;                   // the slots of the step worked on,
+  uint32_t at_fill = kAhead * S::STEP;    // and of the step copied
+  auto advance = [](uint32_t x) { return x == kAhead * S::STEP ? 0u : x + S::STEP; };
+  for (int n = 0; n < steps; n += 2) {
+    __syncwarp();  // the rows of the pair before have been read
+    masks = masks_n;
+    masks_n = __ballot_sync(0xffffffffu, rn >= 0);
+    rows[my_word] = max(rn, 0);
+    rn = look_up(tn);
+    tn = read_key((n >> 1) + 3);
     __syncwarp();
-    const uint32_t mask = n & 1 ? masks >> 16 : masks & 0xffffu;
-    if (mask != 0u) {
-      // S^T = K Q^T, two accumulators
-      float s[2][4];
-      const uint32_t ra = k_at + base, rb = ra + 8 * S::PITCH;
-      const uint32_t rsa = ks_at + base, rsb = rsa + 8 * S::PITCH;
 #pragma unroll
-      for (int c = 0; c < QC; ++c) {
-        uint32_t wa[2], wb[2];
-        load_words(ra + c * 32, wa);
-        load_words(rb + c * 32, wb);
-        const uint32_t sa = e4m3x2_to_f16(load_byte(rsa + c * 4) * 0x0101u);
-        const uint32_t sb = e4m3x2_to_f16(load_byte(rsb + c * 4) * 0x0101u);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t xa[4], xb[4];
-          e2m1x8_to_f16(wa[hf], xa);
-          e2m1x8_to_f16(wb[hf], xb);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t f[4] = {mul_f16x2(xa[2 * i], sa), mul_f16x2(xb[2 * i], sb),
-                                   mul_f16x2(xa[2 * i + 1], sa), mul_f16x2(xb[2 * i + 1], sb)};
-            if (c == 0 && hf == 0)
-              mma_f16_zero(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
-            else
-              mma_f16(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
-          }
-        }
-      }
-      // this thread's values, on their way while the softmax runs
-      const uint32_t v0 = v_at0 + base, v1 = v_at1 + base, v2 = v0 + 8 * S::PITCH,
-                     v3 = v1 + 8 * S::PITCH;
-      uint32_t vw[4][VPT / 8];
-      load_words(v0, vw[0]);
-      load_words(v1, vw[1]);
-      load_words(v2, vw[2]);
-      load_words(v3, vw[3]);
-      uint32_t sc0 = load_byte(v0 + vs_off) | (load_byte(v1 + vs_off) << 8);
-      uint32_t sc1 = load_byte(v2 + vs_off) | (load_byte(v3 + vs_off) << 8);
-
-      float x[4] = {(s[0][0] + s[1][0]) * cs[0], (s[0][1] + s[1][1]) * cs[1],
-                    (s[0][2] + s[1][2]) * cs[0], (s[0][3] + s[1][3]) * cs[1]};
-      if (mask != 0xffffu) {  // row 0 stands in for a missing key: its scale may be NaN
-        if (!((mask >> ka) & 1u)) x[0] = x[1] = -INFINITY;
-        if (!((mask >> (ka + 8)) & 1u)) x[2] = x[3] = -INFINITY;
-        sc0 &= (((mask >> k0) & 1u) * 0xffu) | (((mask >> k1) & 1u) * 0xff00u);
-        sc1 &= (((mask >> (k0 + 8)) & 1u) * 0xffu) | (((mask >> (k1 + 8)) & 1u) * 0xff00u);
-      }
-      float p[4];
-      softmax_step<TOP, MT>(x, m, l, o, p);
-      const __half2 p01 = __floats2half2_rn(p[0], p[1]), p23 = __floats2half2_rn(p[2], p[3]);
-      const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p01));
-      const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p23));
-      const uint32_t s01 = e4m3x2_to_f16(sc0), s23 = e4m3x2_to_f16(sc1);
-      // O^T += V^T P^T
-#pragma unroll
-      for (int w = 0; w < VPT / 8; ++w) {
-        constexpr uint32_t kLo = 0x0f0f0f0fu;
-        uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, two keys each
-        e2m1x8_to_f16((vw[0][w] & kLo) | ((vw[1][w] << 4) & ~kLo), e01);
-        e2m1x8_to_f16(((vw[0][w] >> 4) & kLo) | (vw[1][w] & ~kLo), o01);
-        e2m1x8_to_f16((vw[2][w] & kLo) | ((vw[3][w] << 4) & ~kLo), e23);
-        e2m1x8_to_f16(((vw[2][w] >> 4) & kLo) | (vw[3][w] & ~kLo), o23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t f[4] = {mul_f16x2(e01[i], s01), mul_f16x2(o01[i], s01),
-                                 mul_f16x2(e23[i], s23), mul_f16x2(o23[i], s23)};
-          mma_f16(o[4 * w + i], f, b0, b1);
-        }
-      }
+    for (int half = 0; half < 2; ++half) {
+      if (masks_n != 0u) fill(at_fill, half);
+      cp_async_commit();
+      cp_async_wait<kAhead>();  // this step's copies have landed
+      __syncwarp();
+      const uint32_t mask = half ? masks >> 16 : masks & 0xffffu;
+      if (mask != 0u) step(at_step, mask);
+      __syncwarp();  // its slots may be filled again
+      at_step = advance(at_step);
+      at_fill = advance(at_fill);
     }
-    __syncwarp();  // the step's slots may be filled again
-    base = base == kAhead * S::STEP ? 0 : base + S::STEP;
-    fill_base = fill_base == kAhead * S::STEP ? 0 : fill_base + S::STEP;
-    if (n & 1) masks = masks_n;
   }
   cp_async_wait<0>();  // copies in flight land before the ring is used again
 
@@ -319,7 +343,8 @@ cudaError_t launch(const CacheAttnArgs& a, unsigned grid, cudaStream_t st) {
   const int nw = a.hc * a.nsub * a.kw;
   constexpr size_t ring = (size_t)kQ4Warps * kStages * Slot<DQK, DV>::STEP;
   constexpr size_t merge = (size_t)kQ4Warps * (16 + 8 * DV) * sizeof(float);
-  constexpr size_t smem = ring > merge ? ring : merge;
+  constexpr size_t rows = kQ4Warps * 32 * sizeof(uint32_t);
+  constexpr size_t smem = ring + rows > merge ? ring + rows : merge;
   static_assert(smem <= 112 * 1024, "two CTAs per SM");
   auto kern = cache_attn_q4_kernel<DQK, DV>;
   cudaError_t e =
