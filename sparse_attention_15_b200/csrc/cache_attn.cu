@@ -1,5 +1,6 @@
-// Attention of single query tokens over the paged key/value cache, the headwise gate fused: how a
-// call is laid out over CTAs, and the kernel for bf16 rows (rows held in 4 bits: cache_attn_q4.cu).
+// Attention of single query tokens over the paged key/value cache (bf16 rows, or rows held in 4
+// bits), with a sliding window and visible first tokens, over whole contexts, or over selected
+// keys; the headwise gate fused.
 //
 //   o[h,:] = sum_t p_t v[t,h/G,:],  p = softmax_t(sm_scale * q[h,:] . k[t,h/G,:]),  G = H/HKV
 //
@@ -7,27 +8,92 @@
 // query token has its own key list, so masked keys are never looked at and what they hold (NaN, a
 // page of another sequence, nothing yet) does not matter.
 //
-// One CTA takes a query token, a group of KV heads and a slice of its keys; the slices of one
-// query are merged by launch_split_combine in a fixed order.  Both products run on mma.sync
-// m16n8k16 with the cache as the 16-row operand and the up to 8 query heads of a KV head as the 8
-// columns: S^T = K Q^T [16 keys x 8 heads], O^T += V^T P^T [dims x 8 heads], float32
-// accumulation.  (A tcgen05 tile wants 128 rows that share an operand; here 1 to 8 do.)
+// Products.  Both run on mma.sync m16n8k16 with the cache as the 16-row operand and the up to 8
+// query heads of a KV head as the 8 columns: S^T = K Q^T [16 keys x 8 heads], O^T += V^T P^T
+// [dims x 8 heads], float32 accumulation.  (A tcgen05 tile wants 128 rows that share an operand;
+// here 1 to 8 do, and 4-bit rows have to be widened on their way into the product.)  The
+// contraction order over the dims is free, so a thread takes 16 consecutive dims of a key.
 //
-// bf16 rows: a producer warp turns keys into cache rows through the page table and streams them
-// into a ring of shared-memory slots (1-D bulk copies, mbarrier transaction counts, no
-// multicast); each consumer warp owns one KV head (8 of its query heads) and 16 keys of a stage.
-// The contraction order over the dims is free, so a thread takes 16 consecutive ones of a key.
-// Probabilities are a bf16 pair hi + lo, as one bf16 would be no more exact than the output.
-#include "cache_attn.cuh"
+// Work.  The (query token, group of KV heads) rows, laid end to end in steps of 16 keys, are cut
+// into equal pieces, one per resident CTA, whatever their lengths; a row in several pieces is
+// merged by a second kernel, in order.  Inside a CTA each warp works alone on one KV head (8 of
+// its query heads): it copies its own head's part of 16 keys at a time into its own ring
+// (cp.async, 16 bytes a lane, a step or two ahead), so the loop has no barrier and no producer.
+//
+// What bounds the 4-bit form: 9/16 byte a value, so at 6.5 TB/s 41 values arrive per clock and SM,
+// and each has to be widened to f16 before the tensor cores take it: about 22 instructions per 256
+// values (16 bytes of codes a thread become 16 f16 pairs by 16 conversions and 16 products with
+// the group's scale).  The issue slots and the bandwidth run out together, so everything else is
+// kept short.  The V operand needs two keys in a register: the nibbles of two keys are interleaved
+// before the conversion, which makes pairs of nibbles.  Widening is exact: an e2m1 value times an
+// e4m3 scale has 6 significant bits and stays in f16's normal range.  Queries become f16 after a
+// scaling of each head by a power of two (its largest element to [2^13, 2^14)): exact for every
+// element within 2^-30 of the largest (8 bits into 11), and off by 2^-38 of it at most otherwise.
+// Probabilities are f16 with the running maximum at 2^6 (so terms down to 2^-30 of the largest
+// stay): half a step is 2^-11 each, below the rounding of the output.
+//
+// bf16 rows are bound by the bandwidth.  They are used as they are; probabilities are a bf16 pair
+// hi + lo, as one bf16 would be no more exact than the output.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "cache.cuh"
+#include "kernels.h"
 
 namespace dsa {
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxWarps = 16;     // consumer warps of a CTA
-constexpr int kMaxStages = 8;
-constexpr int kMaxSplit = 64;     // launch_split_combine's limit
+constexpr int kWarps = 8;         // most warps of a CTA
+constexpr int kMinSteps = 4;      // of the least piece
+
+struct CacheAttnArgs {
+  CacheView c;
+  const __nv_bfloat16* q;  // [B,S,H,DQK]
+  const int32_t* pos;      // [B,S]
+  const int32_t* idx;      // [B,S,K] or NULL
+  const __nv_bfloat16* gate;
+  __nv_bfloat16* out;      // [B,S,H,DV]
+  float* part_o;           // [piece, heads of a CTA, DV] (pieces)
+  float* part_ml;          // [piece, heads of a CTA, 2]
+  int gate_mode, S, H, G, K, window, n_first;
+  float qk_scale;          // sm_scale * log2(e) * k_scale
+  int rows, hc, nhg;       // query tokens, KV heads per CTA, CTAs per token and step
+  int nsub, kw;            // warps per KV head (8 query heads each), 16-key groups side by side
+  int grid;                // CTAs that share the steps in pieces; 0: one CTA per token and group
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with C = 0.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -36,134 +102,358 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "memory");
 }
 
+// Asynchronous 16-byte copy to shared memory; a group of them; all but the last N groups landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N words of a slot (aligned to 4N bytes), by their shared-memory address; a byte of one.
+__device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[1]) {
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+__device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[2]) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+}
+__device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t load_byte(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
+// 4 bits: row m of the 16-row operands is key kappa(m) of the step (m and m + 8 alike).  With rows
+// 32 or 96 bytes past a multiple of 128 apart, the K loads (rows g = 0..3 and 4..7 of a half warp)
+// and the V loads (rows 2t, or 2t + 1) both touch four different groups of 8 banks.
+__device__ __forceinline__ int kappa(int g) { return g ^ ((g >> 2) & 1); }
+
+// A key in a warp's ring, and how its pieces of 16 bytes are copied: lane l takes pieces l, l + 32,
+// ... of CYCLE keys' pieces laid end to end, in ROUNDS rounds.
+template <int FMT, int DQK, int DV>
+struct Slot;
+// bf16: K, V.  Rows 16 bytes past a multiple of 128 apart: no bank conflicts.
 template <int DQK, int DV>
-__global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
+struct Slot<0, DQK, DV> {
+  static constexpr int V = DQK * 2, PIECES = (DQK + DV) / 8;
+  static constexpr int CYCLE = PIECES == 16 ? 2 : PIECES == 32 ? 1 : 4;
+  static constexpr int PITCH = (DQK + DV) * 2 + 16;
+};
+// 4 bits: K codes, V codes, then the pieces that hold the K scales and the V scales (4, 8 or 12
+// bytes anywhere in one or two pieces); lanes past the pieces idle.
+template <int DQK, int DV>
+struct Slot<1, DQK, DV> {
+  static constexpr int V = DQK / 2, KS = V + DV / 2, VS = KS + 32;
+  static constexpr int PIECES = (VS + 32) / 16 <= 8 ? 8 : 16;
+  static constexpr int CYCLE = 32 / PIECES;
+  static constexpr int PITCH = (VS + 63) / 64 * 64 + 32;
+  static_assert((VS + 32) / 16 <= 16 && PITCH >= VS + 32, "a key's pieces");
+};
+template <int FMT, int DQK, int DV>
+struct Ring {
+  using S = Slot<FMT, DQK, DV>;
+  static constexpr int STEP = 16 * S::PITCH;  // a step of 16 keys
+  static constexpr int ROUNDS = S::CYCLE * S::PIECES / 32;
+  static constexpr int ROWS = kWarps * 64 * 4;  // a warp's rows of two pairs of steps
+  static constexpr int MERGE = kWarps * (16 + 8 * DV) * 4;
+  static constexpr int fits(int stages) { return ROWS + kWarps * stages * STEP; }
+  // steps copied ahead: two where two CTAs fit an SM so, else one; one CTA: the same
+  static constexpr int HALF = 112 * 1024, WHOLE = 226 * 1024;
+  static constexpr int STAGES = fits(3) <= HALF ? 3 : fits(2) <= HALF ? 2 : fits(3) <= WHOLE ? 3 : 2;
+  static constexpr int PER_SM = fits(STAGES) <= HALF ? 2 : 1;
+  static constexpr int SMEM = fits(STAGES) > MERGE ? fits(STAGES) : MERGE;
+  static_assert(SMEM <= WHOLE && S::CYCLE * S::PIECES % 32 == 0, "ring");
+};
+
+// The keys of a query at position `pos`: n of them, key e being at(e).
+struct KeyList {
+  const int32_t* idx;
+  int n, nf, low;
+  __device__ __forceinline__ int at(int e) const {
+    return idx ? __ldg(idx + e) : (e < nf ? e : low + (e - nf));
+  }
+};
+__device__ __forceinline__ KeyList key_list(const CacheAttnArgs& a, int row, int pos) {
+  KeyList l;
+  l.idx = a.idx ? a.idx + (size_t)row * a.K : nullptr;
+  l.nf = l.low = 0;
+  if (pos < 0) {
+    l.n = 0;
+  } else if (a.idx) {
+    l.n = a.K;
+  } else {
+    const int hi = min(pos, a.c.cap - 1);
+    l.low = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    l.nf = min(min(a.n_first, l.low), a.c.cap);
+    l.n = l.nf + max(0, hi - l.low + 1);
+  }
+  return l;
+}
+// Its steps of kw groups of 16 keys.
+__device__ __forceinline__ int row_steps(const CacheAttnArgs& a, int row) {
+  const int n = key_list(a, row, __ldg(a.pos + row)).n;
+  return (n + 16 * a.kw - 1) / (16 * a.kw);
+}
+
+// Pieces.  The steps of all rows (query tokens), once for each group of heads, are numbered end to
+// end, `each` for a group; CTA c of g takes numbers [c * all / g, (c + 1) * all / g).  Piece numbers
+// grow by one with each CTA and with each row: row r of group hg in CTA c is piece c + hg * R + r.
+__device__ __forceinline__ int ctas_of(const CacheAttnArgs& a, long long all) {
+  const long long most = all / kMinSteps;
+  return (int)(most < 1 ? 1 : most < a.grid ? most : a.grid);
+}
+// The CTA that has step number s.
+__device__ __forceinline__ int cta_of(long long s, long long all, int g) {
+  return (int)(((s + 1) * g - 1) / all);
+}
+
+// Sum over the block of `mine`, and of the threads before this one (blockDim <= 1024).
+__device__ __forceinline__ long long block_scan(long long mine, long long* warp_sums,
+                                                long long* before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  long long base = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) base += warp_sums[w];
+    total += warp_sums[w];
+  }
+  __syncthreads();
+  *before = base + x - mine;
+  return total;
+}
+
+// One 16-key step of the online softmax for the columns 2t, 2t + 1 (heads) of this thread's rows:
+// x = (key g: two columns, key g + 8: two columns) in log2 units, -inf for keys not there.  The
+// running maximum m sits 2^TOP above 1 and is raised once a score passes it by 2^8; p, l and o
+// follow it.
+template <int TOP, int MT>
+__device__ __forceinline__ void softmax_step(const float (&x)[4], float (&m)[2], float (&l)[2],
+                                             float (&o)[MT][4], float (&p)[4]) {
+  float y0 = fmaxf(x[0], x[2]), y1 = fmaxf(x[1], x[3]);
+  if (__any_sync(0xffffffffu, y0 > m[0] + (TOP + 8.0f) || y1 > m[1] + (TOP + 8.0f))) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, d));
+      y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, d));
+    }
+    const float n0 = fmaxf(m[0], y0 - TOP), n1 = fmaxf(m[1], y1 - TOP);
+    const float a0 = m[0] == -INFINITY ? 0.f : ex2_ftz(m[0] - n0);
+    const float a1 = m[1] == -INFINITY ? 0.f : ex2_ftz(m[1] - n1);
+    l[0] *= a0;
+    l[1] *= a1;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      o[i][0] *= a0; o[i][1] *= a1; o[i][2] *= a0; o[i][3] *= a1;
+    }
+    m[0] = n0;
+    m[1] = n1;
+  }
+  // a column without a score above -inf so far has m = -inf: its p must be 0, not NaN
+  const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
+  p[0] = ex2_ftz(x[0] - u0);
+  p[1] = ex2_ftz(x[1] - u1);
+  p[2] = ex2_ftz(x[2] - u0);
+  p[3] = ex2_ftz(x[3] - u1);
+  l[0] += p[0] + p[2];
+  l[1] += p[1] + p[3];
+}
+
+template <int FMT, int DQK, int DV>
+__global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::PER_SM))
+    cache_attn_kernel(const CacheAttnArgs a) {
+  using S = Slot<FMT, DQK, DV>;
+  using R = Ring<FMT, DQK, DV>;
   constexpr int QC = DQK / 64;       // 64-dim chunks: 16 dims per thread each
   constexpr int MT = DV / 16;        // 16-row tiles of O^T
+  constexpr int VPT = DV / 8;        // 4 bits: value dims per thread row
+  constexpr int TOP = FMT == 1 ? 6 : 0;
+  constexpr int AHEAD = R::STAGES - 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + kMaxStages;
-  int* meta = reinterpret_cast<int*>(empty + kMaxStages);  // [stage][8]: -1 = end, 4 mask words
-  float* ml = reinterpret_cast<float*>(smem + 512);        // [warp][8][2]
-  uint8_t* ring = smem + 512 + kMaxWarps * 64;
+  __shared__ long long warp_sums[kWarps];
+  __shared__ int first_row, first_step;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int nw = (blockDim.x >> 5) - 1;
-  const int nhw = nw / a.kw;                 // warps that share a key group
-  const int split = blockIdx.x % a.nsplit;
-  const int hg = (blockIdx.x / a.nsplit) % a.nhg;
-  const int row = blockIdx.x / (a.nsplit * a.nhg);
-  const int hc = a.hc, kv0 = hg * hc;
-  const int ks = a.kw * 16;                  // keys per stage
+  const int nhw = a.hc * a.nsub;
+  const int kg = warp / nhw, hw = warp % nhw;
+  const int sub = hw % a.nsub;
+  const int ncol = min(8, a.G - sub * 8);  // query heads in the 8 columns
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < a.nstages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], nw);
+  // ---- this CTA's steps
+  int row, hg, u0;      // the row, head group and step it starts with
+  long long left;       // its steps
+  if (a.grid == 0) {
+    row = blockIdx.x / a.nhg;
+    hg = blockIdx.x % a.nhg;
+    u0 = 0;
+    left = row_steps(a, row);
+    if (left == 0) left = 1;  // a row without keys gets its zeros from an empty step
+  } else {
+    const int per = (a.rows + blockDim.x - 1) / blockDim.x;
+    const int r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+    long long mine = 0, before;
+    for (int i = r0; i < r1; ++i) mine += row_steps(a, i);
+    const long long each = block_scan(mine, warp_sums, &before);
+    const long long all = each * a.nhg;
+    const int ctas = ctas_of(a, all);
+    if ((int)blockIdx.x >= ctas || all == 0) return;
+    const long long begin = blockIdx.x * all / ctas;
+    left = (blockIdx.x + 1) * all / ctas - begin;
+    hg = (int)(begin / each);
+    const long long in = begin - hg * each;
+    if (before <= in && in < before + mine) {
+      long long s = in - before;
+      int i = r0;
+      for (int n; s >= (n = row_steps(a, i)); ++i) s -= n;
+      first_row = i;
+      first_step = (int)s;
     }
-    fence_mbar_init();
+    __syncthreads();
+    row = first_row;
+    u0 = first_step;
   }
-  __syncthreads();
 
-  const int kb = hc * DQK * 2, vb = hc * DV * 2;  // a slot: this CTA's heads' K, then V
+  const uint32_t ring = smem_u32(smem) + R::ROWS + warp * (R::STAGES * R::STEP);
+  uint32_t* rows = reinterpret_cast<uint32_t*>(smem) + 64 * warp;
+  const uint32_t row_bytes = (uint32_t)a.c.row_bytes;
+  // this lane's pieces of a cycle of keys: the first round's in key cy0, the next rounds' 32 further
+  int cy[R::ROUNDS], at[R::ROUNDS];
+#pragma unroll
+  for (int x = 0; x < R::ROUNDS; ++x) {
+    cy[x] = (lane + 32 * x) / S::PIECES;
+    at[x] = 16 * ((lane + 32 * x) % S::PIECES);
+  }
 
-  if (warp == nw) {
-    // ------------------------------------------------------------- producer
+  for (; left > 0; u0 = 0, hg += row + 1 == a.rows, row = row + 1 == a.rows ? 0 : row + 1) {
     const int pos = __ldg(a.pos + row);
-    const KeyList l = key_list(a, row, pos);
-    int j0, j1;
-    key_slice(l, a.nsplit, split, &j0, &j1);
+    const KeyList list = key_list(a, row, pos);
+    const int n_steps = (list.n + 16 * a.kw - 1) / (16 * a.kw);
+    if (a.grid > 0 && n_steps == 0) continue;
+    const int u1 = (int)min((long long)n_steps, u0 + left);
+    left -= a.grid > 0 ? u1 - u0 : left;
+    const bool alone = u0 == 0 && u1 == n_steps;  // the row's only piece
+    const int j0 = u0 * 16 * a.kw, j1 = min(list.n, u1 * 16 * a.kw);
+    const int kv = hg * a.hc + hw / a.nsub;
+    const int h0 = kv * a.G + sub * 8;
     const int32_t* table = a.c.table + (size_t)(row / a.S) * a.c.max_pages;
-    const uint32_t bytes = (uint32_t)(kb + vb);
-    int fills = 0;
-    bool ok = true;
-    // The keys of a stage (lane: keys lane, lane + 32, ...) are read two stages ahead and their
-    // rows looked up one stage ahead, so that neither load is waited for per stage.
-    int t[4];
-    long long r[4];
-    auto read_keys = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 32 * i + lane;
-        t[i] = k < ks && j < j1 && k < j1 - j ? l.at(j + k) : -1;
-      }
+
+    // ---- keys and rows.  This warp's groups of 16 keys, one per step, come in pairs: lane l looks
+    // after key l & 15 of step l >> 4 of a pair, reads it two pairs ahead and looks its row up one
+    // ahead.
+    const int steps = u1 - u0;
+    const int my_j = j0 + 16 * (kg + a.kw * (lane >> 4)) + (lane & 15);
+    auto read_key = [&](int pair) {  // (below j1 + 2^11: no overflow)
+      const int e = my_j + 32 * a.kw * pair;
+      return e < j1 ? list.at(e) : -1;
     };
-    auto look_up = [&] {
+    auto look_up = [&](int t) { return t <= pos ? cache_row(a.c, table, t) : -1; };
+    int rn = look_up(read_key(0)), tn = read_key(1);
+
+    // ---- copies: where this lane's pieces lie in row 0
+    const int ks0 = cache_ks_off(a.c.HKV, DQK, DV) + kv * (DQK / 16);  // 4 bits: the head's scales
+    const int vs0 = cache_vs_off(a.c.HKV, DQK, DV) + kv * (DV / 16);
+    const uint8_t* from[R::ROUNDS];
+    bool has_piece = true;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = t[i] <= pos ? cache_row(a.c, table, t[i]) : -1;
-    };
-    auto after = [&](int j) { return j1 - j > ks ? j + ks : j1; };
-    read_keys(j0);
-    look_up();
-    read_keys(after(j0));
-    for (int j = j0; ok && j < j1; j = after(j)) {
-      uint32_t m[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m[i] = __ballot_sync(0xffffffffu, r[i] >= 0);
-      const int nvalid = __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
-      const int st = fills % a.nstages;
-      if (nvalid > 0 && fills >= a.nstages)
-        ok = warp_wait(&empty[st], (uint32_t)(fills / a.nstages - 1) & 1u);
-      if (!ok) break;
-      if (nvalid > 0 && lane == 0) {
-        meta[st * 8] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) meta[st * 8 + 1 + i] = (int)m[i];
-        mbar_arrive_expect_tx(&full[st], (uint32_t)nvalid * bytes);
+    for (int x = 0; x < R::ROUNDS; ++x) {
+      int piece = at[x];
+      if constexpr (FMT == 0) {
+        piece += piece < S::V ? kv * (DQK * 2)
+                              : cache_v_off(0, a.c.HKV, DQK) + kv * (DV * 2) - S::V;
+      } else if (piece < S::V) {
+        piece += kv * (DQK / 2);
+      } else if (piece < S::KS) {
+        piece += cache_v_off(1, a.c.HKV, DQK) + kv * (DV / 2) - S::V;
+      } else if (piece < S::VS) {
+        piece += (ks0 & ~15) - S::KS;
+        has_piece = piece < ks0 + DQK / 16;
+      } else {
+        piece += (vs0 & ~15) - S::VS;
+        has_piece = at[x] < S::VS + 32 && piece < vs0 + DV / 16;
       }
-      __syncwarp();
+      from[x] = a.c.pages + (has_piece ? piece : 0);
+    }
+    // A pair's rows in `rows` (two pairs in turn), a step's keys in the order that its copies take
+    // them: key k of the step is word (k % CYCLE) * (16 / CYCLE) + k / CYCLE of its 16.  A key
+    // without a row reads row 0.
+    constexpr int PER = 16 / S::CYCLE;
+    const int my_word = (lane & 16) + (lane & 15) % S::CYCLE * PER + (lane & 15) / S::CYCLE;
+    auto fill = [&](uint32_t stage, int pair_half) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (r[i] < 0) continue;
-        uint8_t* dst = ring + (size_t)(st * ks + 32 * i + lane) * a.pitch;
-        const uint8_t* src = a.c.pages + r[i] * a.c.row_bytes;
-        if (a.nhg == 1) {  // all heads: the whole row
-          bulk_g2s(dst, src, bytes, &full[st]);
-        } else {
-          bulk_g2s(dst, src + (size_t)kv0 * DQK * 2, kb, &full[st]);
-          bulk_g2s(dst + kb, src + cache_v_off(0, a.c.HKV, DQK) + (size_t)kv0 * DV * 2, vb,
-                   &full[st]);
+      for (int x = 0; x < R::ROUNDS; ++x) {
+        const uint32_t dst = ring + stage + cy[x] * S::PITCH + at[x];
+        const uint32_t rows_at = smem_u32(rows) + pair_half * 64 + cy[x] * (PER * 4);
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          uint32_t rk[4];
+          load_words(rows_at + 4 * i, rk);
+          if (has_piece) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              cp_async16(dst + (i + k) * S::CYCLE * S::PITCH,
+                         from[x] + (unsigned long long)rk[k] * row_bytes);
+          }
         }
       }
-      if (nvalid > 0) ++fills;
-      look_up();
-      read_keys(after(after(j)));
-    }
-    // the end mark takes a stage of its own
-    const int st = fills % a.nstages;
-    if (ok && fills >= a.nstages)
-      ok = warp_wait(&empty[st], (uint32_t)(fills / a.nstages - 1) & 1u);
-    if (ok && lane == 0) {
-      meta[st * 8] = -1;
-      mbar_arrive(&full[st]);
-    }
-    // Copies in flight land before the ring is used again or the CTA exits: the last fill of
-    // every stage but the end mark's (whose stage was empty), or of all when a wait gave up.
-    if (lane == 0)
-      for (int f = fills - 1; f >= 0 && f >= fills - a.nstages + (ok ? 1 : 0); --f)
-        drain_wait(&full[f % a.nstages], (uint32_t)(f / a.nstages) & 1u);
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------- consumers
-    const int kg = warp / nhw, hw = warp % nhw;
-    const int kvl = hw / a.nsub, sub = hw % a.nsub;  // local KV head, block of 8 query heads
-    const int ncol = min(8, a.G - sub * 8);          // query heads in the 8 columns
-    const int h0 = (kv0 + kvl) * a.G + sub * 8;
+    };
 
-    // Q^T fragments: column g, dims 64c + 16t .. + 15 of the head
+    // ---- Q^T fragments, column g: dims 64c + 16t .. + 15 of the head
     uint32_t qf[QC][8];
-    const bool has = g < ncol;
-    const uint4* qp = reinterpret_cast<const uint4*>(
-        a.q + ((size_t)row * a.H + (has ? h0 + g : 0)) * DQK + 16 * t4);
+    float cs[2] = {a.qk_scale, a.qk_scale};  // score scale of columns 2t, 2t + 1
+    {
+      const bool has = g < ncol;
+      const uint4* qp = reinterpret_cast<const uint4*>(
+          a.q + ((size_t)row * a.H + (has ? h0 + g : 0)) * DQK + 16 * t4);
 #pragma unroll
-    for (int c = 0; c < QC; ++c)
+      for (int c = 0; c < QC; ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 x = has ? __ldg(qp + c * 8 + i) : make_uint4(0, 0, 0, 0);
-        qf[c][4 * i + 0] = x.x; qf[c][4 * i + 1] = x.y;
-        qf[c][4 * i + 2] = x.z; qf[c][4 * i + 3] = x.w;
-      }
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = has ? __ldg(qp + c * 8 + i) : make_uint4(0, 0, 0, 0);
+          qf[c][4 * i + 0] = x.x; qf[c][4 * i + 1] = x.y;
+          qf[c][4 * i + 2] = x.z; qf[c][4 * i + 3] = x.w;
+        }
+    }
+    if constexpr (FMT == 1) {
+      uint32_t top = 0;  // the largest exponent field of |q|
+#pragma unroll
+      for (int c = 0; c < QC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top = max(top, max((qf[c][i] << 16) & 0x7f800000u, qf[c][i] & 0x7f800000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = max((int)(top >> 23) - 127, -100);  // 2^ex <= max|q| (or less)
+      const float up = __int_as_float((13 - ex + 127) << 23);
+      const float scale = a.qk_scale * __int_as_float((ex - 13 + 127) << 23);
+#pragma unroll
+      for (int c = 0; c < QC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(qf[c][i] << 16) * up,
+                                              __uint_as_float(qf[c][i] & 0xffff0000u) * up);
+          qf[c][i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      cs[0] = __shfl_sync(0xffffffffu, scale, (2 * t4) * 4);
+      cs[1] = __shfl_sync(0xffffffffu, scale, (2 * t4 + 1) * 4);
+    }
+
     float o[MT][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -171,39 +461,116 @@ __global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-    int st = 0;
-    uint32_t phase = 0;
-    while (warp_wait(&full[st], phase)) {
-      if (meta[st * 8] < 0) break;
-      const uint32_t mask = ((uint32_t)meta[st * 8 + 1 + (kg >> 1)] >> ((kg & 1) * 16)) & 0xffffu;
-      if (mask != 0u) {
-        const uint8_t* slot = ring + (size_t)st * ks * a.pitch;
+    // one step: the 16 keys in slots `base` .., of which `mask` have a row
+    const int ka = kappa(g), k0 = kappa(2 * t4), k1 = kappa(2 * t4 + 1);
+    auto step = [&](uint32_t base, uint32_t mask) {
+      if constexpr (FMT == 1) {
+        // this thread's places in a step: key ka's codes and scales, keys k0's and k1's values
+        const uint32_t k_at = ring + ka * S::PITCH + t4 * 8;
+        const uint32_t ks_at = ring + ka * S::PITCH + S::KS + (ks0 & 15) + t4;
+        const uint32_t v_at0 = ring + k0 * S::PITCH + S::V + g * (VPT / 2);
+        const uint32_t v_at1 = ring + k1 * S::PITCH + S::V + g * (VPT / 2);
+        const uint32_t vs_off = S::VS - S::V + (vs0 & 15) + (g * VPT) / 16 - g * (VPT / 2);
+        // S^T = K Q^T, two accumulators
+        float s[2][4];
+        const uint32_t ra = k_at + base, rb = ra + 8 * S::PITCH;
+        const uint32_t rsa = ks_at + base, rsb = rsa + 8 * S::PITCH;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+          uint32_t wa[2], wb[2];
+          load_words(ra + c * 32, wa);
+          load_words(rb + c * 32, wb);
+          const uint32_t sa = e4m3x2_to_f16(load_byte(rsa + c * 4) * 0x0101u);
+          const uint32_t sb = e4m3x2_to_f16(load_byte(rsb + c * 4) * 0x0101u);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t xa[4], xb[4];
+            e2m1x8_to_f16(wa[hf], xa);
+            e2m1x8_to_f16(wb[hf], xb);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t f[4] = {mul_f16x2(xa[2 * i], sa), mul_f16x2(xb[2 * i], sb),
+                                     mul_f16x2(xa[2 * i + 1], sa), mul_f16x2(xb[2 * i + 1], sb)};
+              if (c == 0 && hf == 0)
+                mma_f16_zero(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
+              else
+                mma_f16(s[i], f, qf[c][4 * hf + 2 * i], qf[c][4 * hf + 2 * i + 1]);
+            }
+          }
+        }
+        // this thread's values, on their way while the softmax runs
+        const uint32_t v0 = v_at0 + base, v1 = v_at1 + base, v2 = v0 + 8 * S::PITCH,
+                       v3 = v1 + 8 * S::PITCH;
+        uint32_t vw[4][VPT / 8];
+        load_words(v0, vw[0]);
+        load_words(v1, vw[1]);
+        load_words(v2, vw[2]);
+        load_words(v3, vw[3]);
+        uint32_t sc0 = load_byte(v0 + vs_off) | (load_byte(v1 + vs_off) << 8);
+        uint32_t sc1 = load_byte(v2 + vs_off) | (load_byte(v3 + vs_off) << 8);
+
+        float x[4] = {(s[0][0] + s[1][0]) * cs[0], (s[0][1] + s[1][1]) * cs[1],
+                      (s[0][2] + s[1][2]) * cs[0], (s[0][3] + s[1][3]) * cs[1]};
+        if (mask != 0xffffu) {  // row 0 stands in for a missing key: its scale may be NaN
+          if (!((mask >> ka) & 1u)) x[0] = x[1] = -INFINITY;
+          if (!((mask >> (ka + 8)) & 1u)) x[2] = x[3] = -INFINITY;
+          sc0 &= (((mask >> k0) & 1u) * 0xffu) | (((mask >> k1) & 1u) * 0xff00u);
+          sc1 &= (((mask >> (k0 + 8)) & 1u) * 0xffu) | (((mask >> (k1 + 8)) & 1u) * 0xff00u);
+        }
+        float p[4];
+        softmax_step<TOP, MT>(x, m, l, o, p);
+        const __half2 p01 = __floats2half2_rn(p[0], p[1]), p23 = __floats2half2_rn(p[2], p[3]);
+        const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p01));
+        const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p23));
+        const uint32_t s01 = e4m3x2_to_f16(sc0), s23 = e4m3x2_to_f16(sc1);
+        // O^T += V^T P^T
+#pragma unroll
+        for (int w = 0; w < VPT / 8; ++w) {
+          constexpr uint32_t kLo = 0x0f0f0f0fu;
+          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, two keys each
+          e2m1x8_to_f16((vw[0][w] & kLo) | ((vw[1][w] << 4) & ~kLo), e01);
+          e2m1x8_to_f16(((vw[0][w] >> 4) & kLo) | (vw[1][w] & ~kLo), o01);
+          e2m1x8_to_f16((vw[2][w] & kLo) | ((vw[3][w] << 4) & ~kLo), e23);
+          e2m1x8_to_f16(((vw[2][w] >> 4) & kLo) | (vw[3][w] & ~kLo), o23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {mul_f16x2(e01[i], s01), mul_f16x2(o01[i], s01),
+                                   mul_f16x2(e23[i], s23), mul_f16x2(o23[i], s23)};
+            mma_f16(o[4 * w + i], f, b0, b1);
+          }
+        }
+      } else {
+        // S^T = K Q^T, two accumulators
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-        const uint8_t* ra = slot + (size_t)(kg * 16 + g) * a.pitch + kvl * (DQK * 2) + t4 * 32;
-        const uint8_t* rb = ra + (size_t)8 * a.pitch;
+        const uint32_t ra = ring + base + g * S::PITCH + t4 * 32, rb = ra + 8 * S::PITCH;
 #pragma unroll
         for (int c = 0; c < QC; ++c)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint4 xa = *reinterpret_cast<const uint4*>(ra + c * 128 + hf * 16);
-            const uint4 xb = *reinterpret_cast<const uint4*>(rb + c * 128 + hf * 16);
-            const uint32_t f0[4] = {xa.x, xb.x, xa.y, xb.y};
-            const uint32_t f1[4] = {xa.z, xb.z, xa.w, xb.w};
+            uint32_t xa[4], xb[4];
+            load_words(ra + c * 128 + hf * 16, xa);
+            load_words(rb + c * 128 + hf * 16, xb);
+            const uint32_t f0[4] = {xa[0], xb[0], xa[1], xb[1]};
+            const uint32_t f1[4] = {xa[2], xb[2], xa[3], xb[3]};
             mma_bf16(s[0], f0, qf[c][4 * hf], qf[c][4 * hf + 1]);
             mma_bf16(s[1], f1, qf[c][4 * hf + 2], qf[c][4 * hf + 3]);
           }
-        const bool va = (mask >> g) & 1u, vbk = (mask >> (g + 8)) & 1u;
-        const float cs = a.qk_scale;
-        const float x[4] = {va ? (s[0][0] + s[1][0]) * cs : -INFINITY,
-                            va ? (s[0][1] + s[1][1]) * cs : -INFINITY,
-                            vbk ? (s[0][2] + s[1][2]) * cs : -INFINITY,
-                            vbk ? (s[0][3] + s[1][3]) * cs : -INFINITY};
+        float x[4] = {(s[0][0] + s[1][0]) * cs[0], (s[0][1] + s[1][1]) * cs[1],
+                      (s[0][2] + s[1][2]) * cs[0], (s[0][3] + s[1][3]) * cs[1]};
+        uint32_t k01 = 0xffffffffu, k23 = 0xffffffffu;
+        if (mask != 0xffffu) {  // row 0 stands in for a missing key: it may hold anything
+          if (!((mask >> g) & 1u)) x[0] = x[1] = -INFINITY;
+          if (!((mask >> (g + 8)) & 1u)) x[2] = x[3] = -INFINITY;
+          const uint32_t mk = mask >> (2 * t4);
+          k01 = ((mk & 1u) * 0xffffu) | (((mk >> 1) & 1u) * 0xffff0000u);
+          k23 = (((mk >> 8) & 1u) * 0xffffu) | (((mk >> 9) & 1u) * 0xffff0000u);
+        }
         float p[4];
-        softmax_step<0, MT>(x, m, l, o, p);
+        softmax_step<TOP, MT>(x, m, l, o, p);
         const __nv_bfloat162 h01 = __floats2bfloat162_rn(p[0], p[1]);
         const __nv_bfloat162 h23 = __floats2bfloat162_rn(p[2], p[3]);
         const __nv_bfloat162 r01 = __floats2bfloat162_rn(p[0] - __low2float(h01),
@@ -214,16 +581,8 @@ __global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
         const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&h23));
         const uint32_t c0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&r01));
         const uint32_t c1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&r23));
-        uint32_t k01 = 0xffffffffu, k23 = 0xffffffffu;
-        if (mask != 0xffffu) {  // a slot that was not filled may hold anything
-          k01 = (((mask >> (2 * t4)) & 1u) * 0xffffu) |
-                (((mask >> (2 * t4 + 1)) & 1u) * 0xffff0000u);
-          k23 = (((mask >> (2 * t4 + 8)) & 1u) * 0xffffu) |
-                (((mask >> (2 * t4 + 9)) & 1u) * 0xffff0000u);
-        }
-        const uint32_t v0 = smem_u32(slot) +
-                            (uint32_t)((kg * 16 + (lane & 7) + ((lane >> 4) << 3)) * a.pitch + kb +
-                                       kvl * (DV * 2) + ((lane >> 3) & 1) * 16);
+        const uint32_t v0 = ring + base + ((lane & 7) + ((lane >> 4) << 3)) * S::PITCH + S::V +
+                            ((lane >> 3) & 1) * 16;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           uint32_t f[4];
@@ -233,59 +592,193 @@ __global__ void __maxnreg__(96) cache_attn_bf16_kernel(const CacheAttnArgs a) {
           mma_bf16(o[i], f, c0, c1);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (++st == a.nstages) {
-        st = 0;
-        phase ^= 1u;
-      }
+    };
+
+    // ---- main loop
+    uint32_t masks, masks_n = __ballot_sync(0xffffffffu, rn >= 0);  // keys with a row, of a pair
+    rows[my_word] = max(rn, 0);
+    rn = look_up(tn);
+    tn = read_key(2);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      fill(i * R::STEP, i);
+      cp_async_commit();
     }
-    // this warp's (m, l, O) for the merge
+    uint32_t at_step = 0;                   // the slots of the step worked on,
+    uint32_t at_fill = AHEAD * R::STEP;     // and of the step copied
+    auto advance = [](uint32_t x) { return x == AHEAD * R::STEP ? 0u : x + R::STEP; };
+    int turn = 0;                           // which half of `rows` the pair worked on has
+    for (int n = 0; n < steps; n += 2) {
+      masks = masks_n;
+      masks_n = __ballot_sync(0xffffffffu, rn >= 0);
+      rows[32 * (turn ^ 1) + my_word] = max(rn, 0);
+      rn = look_up(tn);
+      tn = read_key((n >> 1) + 3);
+      __syncwarp();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // step n + half + AHEAD: of this pair (one ahead, half 0), or of the next
+        constexpr bool kOne = AHEAD == 1;
+        const bool next = !kOne || half == 1;
+        if (next ? masks_n != 0u : masks >= 0x10000u)
+          fill(at_fill, 2 * (next ? turn ^ 1 : turn) + (kOne ? half ^ 1 : half));
+        cp_async_commit();
+        cp_async_wait<AHEAD>();  // this step's copies have landed
+        __syncwarp();
+        const uint32_t mask = half ? masks >> 16 : masks & 0xffffu;
+        if (mask != 0u) step(at_step, mask);
+        __syncwarp();  // its slots may be filled again
+        at_step = advance(at_step);
+        at_fill = advance(at_fill);
+      }
+      turn ^= 1;
+    }
+    cp_async_wait<0>();  // copies in flight land before the ring is used again
+
+    // ---- this warp's (m, l, O)
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
       l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
     }
-    __syncthreads();  // every warp is done with the ring, and its copies have landed
-    if (g == 0) *reinterpret_cast<float4*>(ml + warp * 16 + 4 * t4) = make_float4(m[0], l[0], m[1], l[1]);
-    float* c0 = reinterpret_cast<float*>(ring) + (size_t)(warp * 8 + 2 * t4) * DV + g;
+    __syncthreads();
+    float* ml = reinterpret_cast<float*>(smem);    // [warp][8][2]
+    float* ob = ml + kWarps * 16;                  // [warp][8][DV]
+    if (g == 0)
+      *reinterpret_cast<float4*>(ml + warp * 16 + 4 * t4) = make_float4(m[0], l[0], m[1], l[1]);
+    float* c0 = ob + (size_t)(warp * 8 + 2 * t4) * DV;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      c0[16 * i] = o[i][0];
-      c0[16 * i + DV] = o[i][1];
-      c0[16 * i + 8] = o[i][2];
-      c0[16 * i + 8 + DV] = o[i][3];
+      if constexpr (FMT == 1) {
+        const int d = g * VPT + 2 * i;
+        *reinterpret_cast<float2*>(c0 + d) = make_float2(o[i][0], o[i][2]);
+        *reinterpret_cast<float2*>(c0 + DV + d) = make_float2(o[i][1], o[i][3]);
+      } else {
+        const int d = 16 * i + g;
+        c0[d] = o[i][0]; c0[DV + d] = o[i][1]; c0[d + 8] = o[i][2]; c0[DV + d + 8] = o[i][3];
+      }
     }
+    __syncthreads();
+    // ---- merged over the key groups in order: the output row, or this piece of it
+    const int heads = a.hc * a.G;
+    const size_t piece = (size_t)blockIdx.x + (size_t)hg * a.rows + row;
+    for (int i = threadIdx.x; i < heads * (DV / 4); i += blockDim.x) {
+      const int hl = i / (DV / 4), d = (i % (DV / 4)) * 4;
+      const int hh = hl % a.G;
+      const int w0 = (hl / a.G) * a.nsub + (hh >> 3), col = hh & 7;
+      float M = -INFINITY;
+      for (int k = 0; k < a.kw; ++k) M = fmaxf(M, ml[(k * nhw + w0) * 16 + col * 2]);
+      float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < a.kw; ++k) {
+        const int w = k * nhw + w0;
+        const float mk = ml[w * 16 + col * 2];
+        const float f = mk == -INFINITY ? 0.f : ex2_ftz(mk - M);
+        L = fmaf(ml[w * 16 + col * 2 + 1], f, L);
+        const float4 v = *reinterpret_cast<const float4*>(ob + (size_t)(w * 8 + col) * DV + d);
+        x[0] = fmaf(v.x, f, x[0]); x[1] = fmaf(v.y, f, x[1]);
+        x[2] = fmaf(v.z, f, x[2]); x[3] = fmaf(v.w, f, x[3]);
+      }
+      const int h = hg * heads + hl;
+      if (alone) {
+        float f = L > 0.f ? a.c.v_scale / L : 0.f;
+        if (a.gate) f *= gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode);
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * f, x[1] * f);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * f, x[3] * f);
+        uint2 y;
+        y.x = *reinterpret_cast<const uint32_t*>(&y0);
+        y.y = *reinterpret_cast<const uint32_t*>(&y1);
+        *reinterpret_cast<uint2*>(a.out + ((size_t)row * a.H + h) * DV + d) = y;
+      } else {
+        const size_t at_part = piece * heads + hl;
+        *reinterpret_cast<float4*>(a.part_o + at_part * DV + d) =
+            make_float4(x[0], x[1], x[2], x[3]);
+        if (d == 0) {
+          a.part_ml[at_part * 2] = M;
+          a.part_ml[at_part * 2 + 1] = L;
+        }
+      }
+    }
+    __syncthreads();  // the ring may be filled again
   }
-  if (warp == nw) __syncthreads();  // the producer's part of the barrier above
-  __syncthreads();
-  merge_groups<DV>(a, ml, reinterpret_cast<const float*>(ring), nhw, row, split, kv0);
 }
 
-// How a call is laid out over CTAs: KV heads per CTA, warps, stages, key slices.
+// Rows in several pieces, merged in order: one CTA per (query token, head).  Rows without keys get
+// their zeros here.
+template <int DV>
+__global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) {
+  __shared__ long long warp_sums[DV / 32];
+  __shared__ long long s_before;
+  __shared__ float weight[DV];
+  const int row = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int heads = a.hc * a.G, hg = h / heads, hl = h % heads;
+  const int per = (a.rows + DV - 1) / DV;
+  const int r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+  long long mine = 0, before;
+  for (int i = r0; i < r1; ++i) mine += row_steps(a, i);
+  const long long each = block_scan(mine, warp_sums, &before);
+  if (r0 <= row && row < r1) {
+    for (int i = r0; i < row; ++i) before += row_steps(a, i);
+    s_before = before;
+  }
+  __syncthreads();
+  const int n = row_steps(a, row);
+  __nv_bfloat16* out = a.out + ((size_t)row * a.H + h) * DV + threadIdx.x;
+  if (n == 0) {
+    *out = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const long long all = each * a.nhg, s = hg * each + s_before;
+  const int ctas = ctas_of(a, all);
+  const int c0 = cta_of(s, all, ctas), c1 = cta_of(s + n - 1, all, ctas);
+  if (c0 == c1) return;  // one piece: written by its CTA
+  const size_t p0 = (size_t)c0 + (size_t)hg * a.rows + row;
+  const int np = c1 - c0 + 1;
+  const float* ml = a.part_ml + (p0 * heads + hl) * 2;
+  const float* po = a.part_o + (p0 * heads + hl) * DV + threadIdx.x;
+  const size_t step = heads;
+  float M = -INFINITY;
+  for (int p = 0; p < np; ++p) M = fmaxf(M, ml[p * step * 2]);
+  float L = 0.f, x = 0.f;
+  for (int q = 0; q < np; q += DV) {
+    const int nq = min(DV, np - q);
+    __syncthreads();
+    if ((int)threadIdx.x < nq) {
+      const float mp = ml[(q + threadIdx.x) * step * 2];
+      weight[threadIdx.x] = mp == -INFINITY ? 0.f : ex2_ftz(mp - M);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int p = 0; p < nq; ++p) {
+      L = fmaf(ml[(q + p) * step * 2 + 1], weight[p], L);
+      x = fmaf(po[(q + p) * step * DV], weight[p], x);
+    }
+  }
+  float f = L > 0.f ? a.c.v_scale / L : 0.f;
+  if (a.gate) f *= gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode);
+  *out = __float2bfloat16_rn(x * f);
+}
+
+// How a call is laid out over CTAs.
 struct Plan {
-  int hc, nhg, nsub, kw, nw, nstages, pitch, nsplit;
-  size_t smem;
+  int hc, nhg, nsub, kw, nw, grid;
+  size_t pieces;
 };
 
-constexpr size_t kHeadBytes = 512 + kMaxWarps * 64;  // barriers, stage marks, (m, l) of the warps
-
-// bf16: the ring of `hc` KV heads per CTA; false if two stages do not fit.
-bool plan_ring(int hc, int DQK, int DV, Plan* p) {
-  // rows 16 bytes past a multiple of 128 apart: the consumers' loads then meet no bank twice
-  const int part = hc * (DQK + DV) * 2;
-  p->pitch = (part - 16 + 127) / 128 * 128 + 16;
-  const size_t stage = (size_t)p->kw * 16 * p->pitch;
-  const size_t merge = (size_t)p->nw * 8 * DV * 4;
-  // two CTAs per SM where two stages fit in half of its 227 KB, else one
-  size_t budget = p->nw <= 8 ? 113 * 1024 : 226 * 1024;
-  if (kHeadBytes + 2 * stage > budget) budget = 226 * 1024;
-  if (kHeadBytes + 2 * stage > budget || kHeadBytes + merge > budget) return false;
-  const int ns = (int)((budget - kHeadBytes) / stage);
-  p->nstages = ns > kMaxStages ? kMaxStages : ns;
-  const size_t ring = p->nstages * stage;
-  p->smem = kHeadBytes + (ring > merge ? ring : merge);
-  return true;
+template <typename F>
+bool with_dims(int format, int DQK, int DV, F&& f) {
+  auto dims = [&](auto fmt) {
+    constexpr int FMT = decltype(fmt)::value;
+    if (DQK == 64 && DV == 64) return f(Ring<FMT, 64, 64>{}), true;
+    if (DQK == 64 && DV == 128) return f(Ring<FMT, 64, 128>{}), true;
+    if (DQK == 128 && DV == 64) return f(Ring<FMT, 128, 64>{}), true;
+    if (DQK == 128 && DV == 128) return f(Ring<FMT, 128, 128>{}), true;
+    if (DQK == 192 && DV == 64) return f(Ring<FMT, 192, 64>{}), true;
+    if (DQK == 192 && DV == 128) return f(Ring<FMT, 192, 128>{}), true;
+    return false;
+  };
+  return format == 0 ? dims(std::integral_constant<int, 0>{})
+                     : dims(std::integral_constant<int, 1>{});
 }
 
 // Shapes only (no device query), so that workspace sizes are reproducible.
@@ -301,32 +794,16 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   const int nhw = hc * p->nsub;
   p->kw = 8 / nhw;
   p->nw = nhw * p->kw;
-  int resident = 2 * 148;
-  if (format == 0) {
-    if (!plan_ring(hc, DQK, DV, p)) return false;
-    if (p->smem > 113 * 1024) resident = 148;
-  }
-  // key slices: fill the resident CTAs in whole waves, 64 keys a slice at least
+  int resident = 0;
+  if (!with_dims(format, DQK, DV, [&](auto r) { resident = 148 * decltype(r)::PER_SM; }))
+    return false;
+  // Pieces while they may fill the GPU better than the rows do: below two rounds of rows
   const long long ctas = (long long)rows * p->nhg;
-  int best = 1;
-  if (ctas < resident && max_keys > 128) {
-    long long most = (max_keys + 63) / 64;
-    if (most > kMaxSplit) most = kMaxSplit;
-    double best_eff = -1.0;
-    for (int n = 1; n <= (int)most; ++n) {
-      const long long items = ctas * n, waves = (items + resident - 1) / resident;
-      const double eff = (double)items / (double)(waves * resident);
-      if (eff >= 0.95) {
-        best = n;
-        break;
-      }
-      if (eff > best_eff + 1e-9) {
-        best_eff = eff;
-        best = n;
-      }
-    }
+  const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
+  if (ctas < 2 * resident && steps / kMinSteps > ctas) {
+    p->grid = (int)(steps / kMinSteps < resident ? steps / kMinSteps : resident);
+    p->pieces = (size_t)p->grid + (size_t)ctas;
   }
-  p->nsplit = best;
   return true;
 }
 
@@ -340,31 +817,31 @@ long long max_keys_of(const CacheAttnProblem& p) {
   return cap;
 }
 
-template <int DQK, int DV>
-cudaError_t launch_bf16(const CacheAttnArgs& a, const Plan& p, unsigned grid, cudaStream_t st) {
-  auto kern = cache_attn_bf16_kernel<DQK, DV>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+size_t workspace_of(const Plan& pl, const CacheAttnProblem& p) {
+  return pl.pieces * pl.hc * (p.H / p.cache.HKV) * (p.cache.DV + 2) * sizeof(float);
+}
+
+bool plan_of(const CacheAttnProblem& p, Plan* pl) {
+  return make_plan(p.cache.format, p.B * p.S, p.H, p.cache.HKV, p.cache.DQK, p.cache.DV,
+                   max_keys_of(p), pl);
+}
+
+template <int FMT, int DQK, int DV>
+cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cudaStream_t st) {
+  constexpr int smem = Ring<FMT, DQK, DV>::SMEM;
+  auto kern = cache_attn_kernel<FMT, DQK, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // all of the SM's shared memory, or a second CTA would find too little of it
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  kern<<<grid, 32 * (p.nw + 1), p.smem, st>>>(a);
+  const unsigned grid = p.grid > 0 ? (unsigned)p.grid : (unsigned)a.rows * (unsigned)p.nhg;
+  kern<<<grid, 32 * p.nw, smem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.grid == 0) return e;
+  cache_merge_kernel<DV><<<(unsigned)a.rows * a.H, DV, 0, st>>>(a);
   return cudaGetLastError();
-}
-
-cudaError_t launch_dims(const CacheAttnArgs& a, const Plan& p, int rows, cudaStream_t st) {
-  const unsigned grid = (unsigned)rows * (unsigned)(p.nhg * p.nsplit);
-  if (a.c.format == 1) return launch_cache_attn_q4(a, grid, st);
-  const int dqk = a.c.DQK, dv = a.c.DV;
-  if (dqk == 64 && dv == 64) return launch_bf16<64, 64>(a, p, grid, st);
-  if (dqk == 64 && dv == 128) return launch_bf16<64, 128>(a, p, grid, st);
-  if (dqk == 128 && dv == 64) return launch_bf16<128, 64>(a, p, grid, st);
-  if (dqk == 128 && dv == 128) return launch_bf16<128, 128>(a, p, grid, st);
-  if (dqk == 192 && dv == 64) return launch_bf16<192, 64>(a, p, grid, st);
-  if (dqk == 192 && dv == 128) return launch_bf16<192, 128>(a, p, grid, st);
-  return cudaErrorNotSupported;
 }
 
 }  // namespace
@@ -376,41 +853,31 @@ bool cache_attn_supported(int format, int H, int HKV, int DQK, int DV) {
 
 size_t cache_attn_workspace_bytes(const CacheAttnProblem& p) {
   Plan pl;
-  const int rows = p.B * p.S;
-  if (!make_plan(p.cache.format, rows, p.H, p.cache.HKV, p.cache.DQK, p.cache.DV, max_keys_of(p),
-                 &pl) ||
-      pl.nsplit == 1)
-    return 0;
-  return (size_t)rows * pl.nsplit * p.H * (p.cache.DV + 2) * sizeof(float);
+  return plan_of(p, &pl) ? workspace_of(pl, p) : 0;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnProblem& p, void* ws, size_t ws_bytes,
                               cudaStream_t st) {
   Plan pl;
-  const int rows = p.B * p.S;
-  if (!make_plan(p.cache.format, rows, p.H, p.cache.HKV, p.cache.DQK, p.cache.DV, max_keys_of(p),
-                 &pl))
-    return cudaErrorNotSupported;
+  if (!plan_of(p, &pl)) return cudaErrorNotSupported;
   CacheAttnArgs a{};
   a.c = p.cache;
   a.q = static_cast<const __nv_bfloat16*>(p.q);
   a.pos = p.pos; a.idx = p.idx; a.K = p.K; a.window = p.window; a.n_first = p.n_first;
   a.gate = static_cast<const __nv_bfloat16*>(p.gate); a.gate_mode = p.gate_mode;
   a.out = static_cast<__nv_bfloat16*>(p.out);
-  a.S = p.S; a.H = p.H; a.G = p.H / p.cache.HKV;
+  a.S = p.S; a.H = p.H; a.G = p.H / p.cache.HKV; a.rows = p.B * p.S;
   a.qk_scale = p.sm_scale * kLog2e * p.cache.k_scale;
-  a.nsplit = pl.nsplit; a.hc = pl.hc; a.nhg = pl.nhg; a.nsub = pl.nsub; a.kw = pl.kw;
-  a.nstages = pl.nstages; a.pitch = pl.pitch;
-  if (pl.nsplit > 1) {
-    const size_t need = (size_t)rows * pl.nsplit * p.H * (p.cache.DV + 2) * sizeof(float);
-    if (ws == nullptr || ws_bytes < need) return cudaErrorInvalidValue;
+  a.hc = pl.hc; a.nhg = pl.nhg; a.nsub = pl.nsub; a.kw = pl.kw; a.grid = pl.grid;
+  if (pl.grid > 0) {
+    if (ws == nullptr || ws_bytes < workspace_of(pl, p)) return cudaErrorInvalidValue;
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = a.part_o + (size_t)rows * pl.nsplit * p.H * p.cache.DV;
+    a.part_ml = a.part_o + pl.pieces * pl.hc * a.G * p.cache.DV;
   }
-  const cudaError_t e = launch_dims(a, pl, rows, st);
-  if (e != cudaSuccess || pl.nsplit == 1) return e;
-  return launch_split_combine(1, a.part_o, a.part_ml, rows, pl.nsplit, p.H, p.cache.DV, p.gate,
-                              p.gate_mode, p.out, st);
+  cudaError_t e = cudaErrorNotSupported;
+  with_dims(p.cache.format, p.cache.DQK, p.cache.DV,
+            [&](auto ring) { e = launch(a, pl, ring, st); });
+  return e;
 }
 
 }  // namespace dsa
