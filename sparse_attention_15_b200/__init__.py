@@ -506,47 +506,39 @@ class Cache:
                              f"{fmt} kv_heads={kv_heads} dqk={dqk} dv={dv}")
         if table.device != pages.device:
             raise ValueError("pages and table are on different devices")
-        self.pages, self.table = pages, table
+        self.pages, self.table, self.device = pages, table, pages.device
         self.kv_heads, self.dqk, self.dv = int(kv_heads), int(dqk), int(dv)
         self.args = CacheArgs(format=CACHE_FORMAT[fmt], n_pages=pages.shape[0],
                               page_size=pages.shape[1], max_pages=table.shape[1],
                               HKV=self.kv_heads, DQK=self.dqk, DV=self.dv,
                               k_scale=float(k_scale), v_scale=float(v_scale),
                               pages=pages.data_ptr(), table=table.data_ptr())
+        self.ref = ctypes.byref(self.args)
+        self._workspaces = {}  # workspace bytes by the sizes of a call
 
+    def _rows(self, pos):
+        """(B, S) of a call with positions pos, which must suit the table and the current device."""
+        if pos.dim() != 2 or pos.shape[0] != self.table.shape[0]:
+            raise ValueError(f"pos is [B, S] with B = {self.table.shape[0]} (the table's rows)")
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.device}, which is not the current device")
+        self._takes("pos", pos, pos.shape, torch.int32)
+        return pos.shape
 
-def _cache_check(cache, pos, shapes, types):
-    """The tensors of a cache call: contiguous, on the cache's device, which is the current one, of
-    the shapes and types named (None: not given).  Returns (B, S)."""
-    if pos.dim() != 2 or pos.shape[0] != cache.table.shape[0]:
-        raise ValueError(f"pos is [B, S] with B = {cache.table.shape[0]} (the table's rows)")
-    dev = cache.pages.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, which is not the current device")
-    for name, (t, shape) in shapes.items():
+    def _takes(self, name, t, shape, dtype=torch.bfloat16):
+        """A call's tensor: contiguous, of this shape and type, on the cache's device; its address
+        (None: not given)."""
         if t is None:
-            continue
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != types.get(name, torch.bfloat16):
-            raise ValueError(f"{name} has dtype {t.dtype}")
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: libdsa takes contiguous CUDA tensors on the cache's device")
+            return None
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected a "
+                             f"contiguous {tuple(shape)} {dtype} on {self.device}")
+        return t.data_ptr()
 
 
-def _cache_workspace(nbytes, device, ws, stream):
-    """The caller's workspace, or one of this call that its stream keeps until it is done."""
-    if nbytes == 0:
-        return None
-    if ws is not None:
-        _dev(ws)
-        if ws.numel() * ws.element_size() < nbytes:
-            raise ValueError(f"the workspace has fewer than {nbytes} bytes")
-        return ws
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+def _raw_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
 def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=None, k_out=None,
@@ -556,70 +548,87 @@ def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=
     "interleaved": pairs (2j, 2j+1), or "half": pairs (j, j + len)), and rotates the same tokens'
     queries q [B,S,H,DQK] into q_out (may be q).  k_out, if given, receives the rotated keys (may be
     k).  Returns (rotated queries or None, k_out); with rope "off" q comes back as it is."""
-    B, S = pos.shape
-    KH = cache.kv_heads
-    H = KH if q is None else q.shape[2]
-    rotated = rope != "off"
-    if not rotated and q_out is not None:
-        raise ValueError("q_out goes with a rotation")
-    qs = (B, S, H, cache.dqk)
-    f = inv_freq if rotated else None
-    if rotated and f is None:
-        raise ValueError("a rotation needs inv_freq")
-    _cache_check(cache, pos, {
-        "pos": (pos, (B, S)), "k": (k, (B, S, KH, cache.dqk)), "v": (v, (B, S, KH, cache.dv)),
-        "q": (q, qs), "q_out": (q_out, qs), "k_out": (k_out, (B, S, KH, cache.dqk)),
-        "inv_freq": (f, (0 if f is None else f.numel(),))},
-        {"pos": torch.int32, "inv_freq": torch.float32})
-    if rotated and q is not None and q_out is None:
-        q_out = torch.empty_like(q)
-    _check(lib().dsa_cache_append(
-        ctypes.byref(cache.args), _ptr(pos), _ptr(k), _ptr(v), ROPE[rope],
-        2 * f.numel() if rotated else 0, _ptr(f), B, S, H, _ptr(q) if rotated else None,
-        _ptr(q_out), _ptr(k_out), _stream(stream)))
-    return (q_out if rotated else q), k_out
+    B, S = cache._rows(pos)
+    takes = cache._takes
+    ks = (B, S, cache.kv_heads, cache.dqk)
+    kp, vp = takes("k", k, ks), takes("v", v, (B, S, cache.kv_heads, cache.dv))
+    ko = takes("k_out", k_out, ks)
+    H, qp, qo, fp, rot = cache.kv_heads, None, None, None, 0
+    if rope == "off":
+        if q_out is not None:
+            raise ValueError("q_out goes with a rotation")
+        q_out = q
+    else:
+        if inv_freq is None:
+            raise ValueError("a rotation needs inv_freq")
+        fp, rot = takes("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32), inv_freq.numel()
+        if q is not None:
+            H = q.shape[2] if q.dim() == 4 else 0
+            qs = (B, S, H, cache.dqk)
+            qp = takes("q", q, qs)
+            if q_out is None:
+                q_out = torch.empty_like(q)
+            qo = takes("q_out", q_out, qs)
+        elif q_out is not None:
+            raise ValueError("q_out goes with q")
+    _check(lib().dsa_cache_append(cache.ref, pos.data_ptr(), kp, vp, ROPE[rope], 2 * rot, fp, B, S,
+                                  H, qp, qo, ko, _raw_stream(stream, cache.device)))
+    return q_out, k_out
 
 
 def dsa_cache_read(cache, pos, k=None, v=None, stream=None):
     """The tokens at pos [B,S] as the cache holds them: (k [B,S,HKV,DQK], v [B,S,HKV,DV]) in bf16,
     zeros where it has no row."""
-    B, S = pos.shape
+    B, S = cache._rows(pos)
     ks, vs = (B, S, cache.kv_heads, cache.dqk), (B, S, cache.kv_heads, cache.dv)
     if k is None:
-        k = torch.empty(ks, dtype=torch.bfloat16, device=cache.pages.device)
+        k = torch.empty(ks, dtype=torch.bfloat16, device=cache.device)
     if v is None:
-        v = torch.empty(vs, dtype=torch.bfloat16, device=cache.pages.device)
-    _cache_check(cache, pos, {"pos": (pos, (B, S)), "k": (k, ks), "v": (v, vs)},
-                 {"pos": torch.int32})
-    _check(lib().dsa_cache_read(ctypes.byref(cache.args), _ptr(pos), B, S, _ptr(k), _ptr(v),
-                                _stream(stream)))
+        v = torch.empty(vs, dtype=torch.bfloat16, device=cache.device)
+    _check(lib().dsa_cache_read(cache.ref, pos.data_ptr(), B, S, cache._takes("k", k, ks),
+                                cache._takes("v", v, vs), _raw_stream(stream, cache.device)))
     return k, v
 
 
 def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, out, ws, stream):
-    B, S = pos.shape
-    H = q.shape[2]
+    B, S = cache._rows(pos)
+    takes = cache._takes
+    H = q.shape[2] if q.dim() == 4 else 0
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
-    os_ = (B, S, H, cache.dv)
+    qp = takes("q", q, (B, S, H, cache.dqk))
+    gp = takes("gate", gate, (B, S, H))
     if out is None:
-        out = torch.empty(os_, dtype=torch.bfloat16, device=cache.pages.device)
-    K = 0 if idx is None else idx.shape[-1]
-    _cache_check(cache, pos, {
-        "pos": (pos, (B, S)), "q": (q, (B, S, H, cache.dqk)), "gate": (gate, (B, S, H)),
-        "out": (out, os_), "idx": (idx, (B, S, K))}, {"pos": torch.int32, "idx": torch.int32})
-    L, c = lib(), ctypes.byref(cache.args)
-    if idx is None:
-        nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, int(window), int(n_first)))
-        ws = _cache_workspace(nbytes, out.device, ws, stream)
-        _check(L.dsa_cache_attn(c, _ptr(q), _ptr(pos), int(window), int(n_first), _ptr(gate), gm,
-                                float(sm_scale), B, S, H, _ptr(out), _ptr(ws), nbytes,
-                                _stream(stream)))
+        out = torch.empty((B, S, H, cache.dv), dtype=torch.bfloat16, device=cache.device)
+        op = out.data_ptr()
     else:
-        nbytes = int(L.dsa_cache_sparse_attn_workspace_bytes(c, B, S, H, K))
-        ws = _cache_workspace(nbytes, out.device, ws, stream)
-        _check(L.dsa_cache_sparse_attn(c, _ptr(q), _ptr(pos), _ptr(idx), K, _ptr(gate), gm,
-                                       float(sm_scale), B, S, H, _ptr(out), _ptr(ws), nbytes,
-                                       _stream(stream)))
+        op = takes("out", out, (B, S, H, cache.dv))
+    L, c = lib(), cache.ref
+    K = 0 if idx is None else idx.shape[-1]
+    ip = takes("idx", idx, (B, S, K), torch.int32)
+    sizes = (B, S, H, K, window, n_first)
+    nbytes = cache._workspaces.get(sizes)
+    if nbytes is None:
+        nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, int(window), int(n_first))
+                     if idx is None else L.dsa_cache_sparse_attn_workspace_bytes(c, B, S, H, K))
+        cache._workspaces[sizes] = nbytes
+    wp = None
+    if nbytes:
+        if ws is None:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            if stream is not None:
+                ws.record_stream(stream)  # not to be handed out again before that stream is done
+        elif not ws.is_contiguous() or ws.device != cache.device or \
+                ws.numel() * ws.element_size() < nbytes:
+            raise ValueError(f"ws is a contiguous tensor of at least {nbytes} bytes on "
+                             f"{cache.device}")
+        wp = ws.data_ptr()
+    st = _raw_stream(stream, cache.device)
+    if idx is None:
+        _check(L.dsa_cache_attn(c, qp, pos.data_ptr(), int(window), int(n_first), gp, gm,
+                                float(sm_scale), B, S, H, op, wp, nbytes, st))
+    else:
+        _check(L.dsa_cache_sparse_attn(c, qp, pos.data_ptr(), ip, K, gp, gm, float(sm_scale), B, S,
+                                       H, op, wp, nbytes, st))
     return out
 
 
