@@ -47,7 +47,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 8;         // most warps of a CTA
-constexpr int kMinSteps = 4;      // of the least piece
 
 struct CacheAttnArgs {
   CacheView c;
@@ -63,6 +62,7 @@ struct CacheAttnArgs {
   int rows, hc, nhg;       // query tokens, KV heads per CTA, CTAs per token and step
   int nsub, kw;            // warps per KV head (8 query heads each), 16-key groups side by side
   int grid;                // CTAs that share the steps in pieces; 0: one CTA per token and group
+  int least;               // steps of the least piece
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -209,7 +209,7 @@ __device__ __forceinline__ int row_steps(const CacheAttnArgs& a, int row) {
 // end, `each` for a group; CTA c of g takes numbers [c * all / g, (c + 1) * all / g).  Piece numbers
 // grow by one with each CTA and with each row: row r of group hg in CTA c is piece c + hg * R + r.
 __device__ __forceinline__ int ctas_of(const CacheAttnArgs& a, long long all) {
-  const long long most = all / kMinSteps;
+  const long long most = all / a.least;
   return (int)(most < 1 ? 1 : most < a.grid ? most : a.grid);
 }
 // The CTA that has step number s.
@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::PER_SM))
   __shared__ long long warp_sums[kWarps];
   __shared__ int first_row, first_step;
 
+  // the merge kernel may start: it waits for this grid's end before it reads the pieces
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int nhw = a.hc * a.nsub;
@@ -723,6 +725,8 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
   }
   __syncthreads();
   const int n = row_steps(a, row);
+  // the pieces are written (every CTA waits, so that this grid never ends before the one it merges)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __nv_bfloat16* out = a.out + ((size_t)row * a.H + h) * DV + threadIdx.x;
   if (n == 0) {
     *out = __float2bfloat16_rn(0.f);
@@ -761,7 +765,7 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
 
 // How a call is laid out over CTAs.
 struct Plan {
-  int hc, nhg, nsub, kw, nw, grid;
+  int hc, nhg, nsub, kw, nw, grid, least;
   size_t pieces;
 };
 
@@ -797,11 +801,15 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   int resident = 0;
   if (!with_dims(format, DQK, DV, [&](auto r) { resident = 148 * decltype(r)::PER_SM; }))
     return false;
-  // Pieces while they may fill the GPU better than the rows do: below two rounds of rows
+  // Pieces while they may fill the GPU better than the rows do: below two rounds of rows.  A piece
+  // costs as much as some steps (its queries, the first copies' latency, its merge), so it has 8 of
+  // them, or 4 where the rows leave more than half of the SMs idle (20 tokens with 16 steps in 5
+  // groups: 21.5 us with 8, 30.7 us with 4; one token with 33 steps: 18.6 us and 16.5 us).
   const long long ctas = (long long)rows * p->nhg;
+  p->least = ctas >= 74 ? 8 : 4;
   const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
-  if (ctas < 2 * resident && steps / kMinSteps > ctas) {
-    p->grid = (int)(steps / kMinSteps < resident ? steps / kMinSteps : resident);
+  if (ctas < 2 * resident && steps / p->least > ctas) {
+    p->grid = (int)(steps / p->least < resident ? steps / p->least : resident);
     p->pieces = (size_t)p->grid + (size_t)ctas;
   }
   return true;
@@ -840,8 +848,17 @@ cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cu
   kern<<<grid, 32 * p.nw, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.grid == 0) return e;
-  cache_merge_kernel<DV><<<(unsigned)a.rows * a.H, DV, 0, st>>>(a);
-  return cudaGetLastError();
+  // launched beside the pieces (programmatic dependence), so that its start costs no time after them
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.rows * a.H);
+  cfg.blockDim = dim3(DV);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<DV>, a);
 }
 
 }  // namespace
@@ -869,6 +886,7 @@ cudaError_t launch_cache_attn(const CacheAttnProblem& p, void* ws, size_t ws_byt
   a.S = p.S; a.H = p.H; a.G = p.H / p.cache.HKV; a.rows = p.B * p.S;
   a.qk_scale = p.sm_scale * kLog2e * p.cache.k_scale;
   a.hc = pl.hc; a.nhg = pl.nhg; a.nsub = pl.nsub; a.kw = pl.kw; a.grid = pl.grid;
+  a.least = pl.least;
   if (pl.grid > 0) {
     if (ws == nullptr || ws_bytes < workspace_of(pl, p)) return cudaErrorInvalidValue;
     a.part_o = static_cast<float*>(ws);
