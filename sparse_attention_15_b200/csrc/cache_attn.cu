@@ -165,14 +165,19 @@ struct Ring {
   static constexpr int STEP = 16 * S::PITCH;  // a step of 16 keys
   static constexpr int ROUNDS = S::CYCLE * S::PIECES / 32;
   static constexpr int ROWS = kWarps * 64 * 4;  // a warp's rows of two pairs of steps
-  static constexpr int MERGE = kWarps * (16 + 8 * DV) * 4;
-  static constexpr int fits(int stages) { return ROWS + kWarps * stages * STEP; }
-  // steps copied ahead: two where two CTAs fit an SM so, else one; one CTA: the same
-  static constexpr int HALF = 112 * 1024, WHOLE = 226 * 1024;
-  static constexpr int STAGES = fits(3) <= HALF ? 3 : fits(2) <= HALF ? 2 : fits(3) <= WHOLE ? 3 : 2;
-  static constexpr int PER_SM = fits(STAGES) <= HALF ? 2 : 1;
-  static constexpr int SMEM = fits(STAGES) > MERGE ? fits(STAGES) : MERGE;
-  static_assert(SMEM <= WHOLE && S::CYCLE * S::PIECES % 32 == 0, "ring");
+  static constexpr int fits(int stages, int warps) { return ROWS + warps * stages * STEP; }
+  // Warps that a CTA should have, and steps in a warp's ring (one worked on): two CTAs per SM, of 8
+  // warps if that leaves two steps or more, else of 4.  (An SM has 228 KB, 1 KB of them for each
+  // CTA's own use.)
+  static constexpr int HALF = 113 * 1024, WHOLE = 226 * 1024;
+  static constexpr int WARPS = fits(2, 8) <= HALF ? 8 : 4;
+  static constexpr int STAGES = fits(3, WARPS) <= HALF ? 3 : 2;
+  static constexpr int smem(int warps) {
+    const int merge = warps * (16 + 8 * DV) * 4;
+    return fits(STAGES, warps) > merge ? fits(STAGES, warps) : merge;
+  }
+  static_assert(smem(WARPS) <= HALF && smem(kWarps) <= WHOLE && S::CYCLE * S::PIECES % 32 == 0,
+                "ring");
 };
 
 // The keys of a query at position `pos`: n of them, key e being at(e).
@@ -276,7 +281,7 @@ __device__ __forceinline__ void softmax_step(const float (&x)[4], float (&m)[2],
 }
 
 template <int FMT, int DQK, int DV>
-__global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::PER_SM))
+__global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::WARPS == 8 ? 2 : 1))
     cache_attn_kernel(const CacheAttnArgs a) {
   using S = Slot<FMT, DQK, DV>;
   using R = Ring<FMT, DQK, DV>;
@@ -646,7 +651,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::PER_SM))
     }
     __syncthreads();
     float* ml = reinterpret_cast<float*>(smem);    // [warp][8][2]
-    float* ob = ml + kWarps * 16;                  // [warp][8][DV]
+    float* ob = ml + (blockDim.x >> 5) * 16;       // [warp][8][DV]
     if (g == 0)
       *reinterpret_cast<float4*>(ml + warp * 16 + 4 * t4) = make_float4(m[0], l[0], m[1], l[1]);
     float* c0 = ob + (size_t)(warp * 8 + 2 * t4) * DV;
@@ -785,22 +790,27 @@ bool with_dims(int format, int DQK, int DV, F&& f) {
                      : dims(std::integral_constant<int, 1>{});
 }
 
+constexpr int kPiece = 4;
+
 // Shapes only (no device query), so that workspace sizes are reproducible.
 bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long max_keys, Plan* p) {
   *p = Plan{};
   p->nsub = (H / HKV + 7) / 8;
-  // KV heads per CTA: the most that divide HKV and keep 6 to 8 warps busy, more than one warp per
+  int warps = 0;
+  if (!with_dims(format, DQK, DV, [&](auto r) { warps = decltype(r)::WARPS; })) return false;
+  if (p->nsub > warps) warps = kWarps;
+  // KV heads per CTA: the most that divide HKV and keep 3 of 4 warps busy, more than one warp per
   // head taking different keys
-  int hc = 8 / p->nsub;
-  while (HKV % hc != 0 || (hc > 1 && hc * p->nsub * (8 / (hc * p->nsub)) < 6)) --hc;
+  int hc = warps / p->nsub;
+  while (HKV % hc != 0 || (hc > 1 && 4 * hc * p->nsub * (warps / (hc * p->nsub)) < 3 * warps)) --hc;
   p->hc = hc;
   p->nhg = HKV / hc;
   const int nhw = hc * p->nsub;
-  p->kw = 8 / nhw;
+  p->kw = warps / nhw;
   p->nw = nhw * p->kw;
-  int resident = 0;
-  if (!with_dims(format, DQK, DV, [&](auto r) { resident = 148 * decltype(r)::PER_SM; }))
-    return false;
+  int smem = 0;
+  with_dims(format, DQK, DV, [&](auto r) { smem = decltype(r)::smem(p->nw); });
+  const int resident = 148 * (smem <= 113 * 1024 ? 2 : 1);
   // Pieces while they may fill the GPU better than the rows do: below two rounds of rows.  A piece
   // costs as much as some steps (its queries, the first copies' latency, its merge), so it has 8 of
   // them, or 4 where the rows leave more than half of the SMs idle (20 tokens with 16 steps in 5
@@ -810,6 +820,11 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
   if (ctas < 2 * resident && steps / p->least > ctas) {
     p->grid = (int)(steps / p->least < resident ? steps / p->least : resident);
+    // A cut inside a CTA's share costs a second piece, about kPiece steps: a grid that cuts rows of
+    // one length into whole shares may be faster, although smaller (64 windows of 33 steps in 2
+    // groups: 44.6 us on 256 CTAs, 47.9 us on 296; 16 rows of 128 steps in 8: 130 us on 296).
+    const long long whole = ctas * (p->grid / ctas);
+    if (whole > 0 && steps / whole + kPiece < steps / p->grid + 2 * kPiece) p->grid = (int)whole;
     p->pieces = (size_t)p->grid + (size_t)ctas;
   }
   return true;
@@ -836,7 +851,7 @@ bool plan_of(const CacheAttnProblem& p, Plan* pl) {
 
 template <int FMT, int DQK, int DV>
 cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cudaStream_t st) {
-  constexpr int smem = Ring<FMT, DQK, DV>::SMEM;
+  const int smem = Ring<FMT, DQK, DV>::smem(p.nw);
   auto kern = cache_attn_kernel<FMT, DQK, DV>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // all of the SM's shared memory, or a second CTA would find too little of it
