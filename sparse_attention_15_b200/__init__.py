@@ -514,6 +514,7 @@ class Cache:
                               k_scale=float(k_scale), v_scale=float(v_scale),
                               pages=pages.data_ptr(), table=table.data_ptr())
         self.ref = ctypes.byref(self.args)
+        self._bf16 = torch.empty(0, dtype=torch.bfloat16, device=self.device)  # outputs' kind
         self._workspaces = {}  # workspace bytes by the sizes of a call
 
     def _rows(self, pos):
@@ -538,7 +539,8 @@ class Cache:
 
 
 def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    # (the handle alone: building a Stream object takes 2 us, a tenth of a decode call)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=None, k_out=None,
@@ -582,9 +584,9 @@ def dsa_cache_read(cache, pos, k=None, v=None, stream=None):
     B, S = cache._rows(pos)
     ks, vs = (B, S, cache.kv_heads, cache.dqk), (B, S, cache.kv_heads, cache.dv)
     if k is None:
-        k = torch.empty(ks, dtype=torch.bfloat16, device=cache.device)
+        k = cache._bf16.new_empty(ks)
     if v is None:
-        v = torch.empty(vs, dtype=torch.bfloat16, device=cache.device)
+        v = cache._bf16.new_empty(vs)
     _check(lib().dsa_cache_read(cache.ref, pos.data_ptr(), B, S, cache._takes("k", k, ks),
                                 cache._takes("v", v, vs), _raw_stream(stream, cache.device)))
     return k, v
@@ -598,7 +600,7 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
     qp = takes("q", q, (B, S, H, cache.dqk))
     gp = takes("gate", gate, (B, S, H))
     if out is None:
-        out = torch.empty((B, S, H, cache.dv), dtype=torch.bfloat16, device=cache.device)
+        out = cache._bf16.new_empty((B, S, H, cache.dv))
         op = out.data_ptr()
     else:
         op = takes("out", out, (B, S, H, cache.dv))
