@@ -62,7 +62,7 @@ struct CacheAttnArgs {
   int rows, hc, nhg;       // query tokens, KV heads per CTA, CTAs per token and step
   int nsub, kw;            // warps per KV head (8 query heads each), 16-key groups side by side
   int grid;                // CTAs that share the steps in pieces; 0: one CTA per token and group
-  int least;               // steps of the least piece
+  int least_log;           // log2 of the steps of the least piece
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -214,12 +214,18 @@ __device__ __forceinline__ int row_steps(const CacheAttnArgs& a, int row) {
 // end, `each` for a group; CTA c of g takes numbers [c * all / g, (c + 1) * all / g).  Piece numbers
 // grow by one with each CTA and with each row: row r of group hg in CTA c is piece c + hg * R + r.
 __device__ __forceinline__ int ctas_of(const CacheAttnArgs& a, long long all) {
-  const long long most = all / a.least;
+  const long long most = all >> a.least_log;
   return (int)(most < 1 ? 1 : most < a.grid ? most : a.grid);
+}
+// a / b for a >= 0, b > 0: by a 32-bit division (a fifth of the time) where both fit, as they nearly
+// always do.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 // The CTA that has step number s.
 __device__ __forceinline__ int cta_of(long long s, long long all, int g) {
-  return (int)(((s + 1) * g - 1) / all);
+  return (int)quotient((s + 1) * g - 1, all);
 }
 
 // Sum over the block of `mine`, and of the threads before this one (blockDim <= 1024).
@@ -321,9 +327,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::WARPS == 8 ?
     const long long all = each * a.nhg;
     const int ctas = ctas_of(a, all);
     if ((int)blockIdx.x >= ctas || all == 0) return;
-    const long long begin = blockIdx.x * all / ctas;
-    left = (blockIdx.x + 1) * all / ctas - begin;
-    hg = (int)(begin / each);
+    const long long begin = quotient(blockIdx.x * all, ctas);
+    left = quotient((blockIdx.x + 1) * all, ctas) - begin;
+    hg = (int)quotient(begin, each);
     const long long in = begin - hg * each;
     if (before <= in && in < before + mine) {
       long long s = in - before;
@@ -420,6 +426,18 @@ __global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::WARPS == 8 ?
         }
       }
     };
+
+    // ---- the first steps' copies, on their way while the queries are read
+    uint32_t masks, masks_n = __ballot_sync(0xffffffffu, rn >= 0);  // keys with a row, of a pair
+    rows[my_word] = max(rn, 0);
+    rn = look_up(tn);
+    tn = read_key(2);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      fill(i * R::STEP, i);
+      cp_async_commit();
+    }
 
     // ---- Q^T fragments, column g: dims 64c + 16t .. + 15 of the head
     uint32_t qf[QC][8];
@@ -602,16 +620,6 @@ __global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::WARPS == 8 ?
     };
 
     // ---- main loop
-    uint32_t masks, masks_n = __ballot_sync(0xffffffffu, rn >= 0);  // keys with a row, of a pair
-    rows[my_word] = max(rn, 0);
-    rn = look_up(tn);
-    tn = read_key(2);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      fill(i * R::STEP, i);
-      cp_async_commit();
-    }
     uint32_t at_step = 0;                   // the slots of the step worked on,
     uint32_t at_fill = AHEAD * R::STEP;     // and of the step copied
     auto advance = [](uint32_t x) { return x == AHEAD * R::STEP ? 0u : x + R::STEP; };
@@ -770,7 +778,7 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
 
 // How a call is laid out over CTAs.
 struct Plan {
-  int hc, nhg, nsub, kw, nw, grid, least;
+  int hc, nhg, nsub, kw, nw, grid, least_log;
   size_t pieces;
 };
 
@@ -816,10 +824,10 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   // them, or 4 where the rows leave more than half of the SMs idle (20 tokens with 16 steps in 5
   // groups: 21.5 us with 8, 30.7 us with 4; one token with 33 steps: 18.6 us and 16.5 us).
   const long long ctas = (long long)rows * p->nhg;
-  p->least = ctas >= 74 ? 8 : 4;
+  p->least_log = ctas >= 74 ? 3 : 2;
   const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
-  if (ctas < 2 * resident && steps / p->least > ctas) {
-    p->grid = (int)(steps / p->least < resident ? steps / p->least : resident);
+  if (ctas < 2 * resident && (steps >> p->least_log) > ctas) {
+    p->grid = (int)((steps >> p->least_log) < resident ? (steps >> p->least_log) : resident);
     // A cut inside a CTA's share costs a second piece, about kPiece steps: a grid that cuts rows of
     // one length into whole shares may be faster, although smaller (64 windows of 33 steps in 2
     // groups: 44.6 us on 256 CTAs, 47.9 us on 296; 16 rows of 128 steps in 8: 130 us on 296).
@@ -901,7 +909,7 @@ cudaError_t launch_cache_attn(const CacheAttnProblem& p, void* ws, size_t ws_byt
   a.S = p.S; a.H = p.H; a.G = p.H / p.cache.HKV; a.rows = p.B * p.S;
   a.qk_scale = p.sm_scale * kLog2e * p.cache.k_scale;
   a.hc = pl.hc; a.nhg = pl.nhg; a.nsub = pl.nsub; a.kw = pl.kw; a.grid = pl.grid;
-  a.least = pl.least;
+  a.least_log = pl.least_log;
   if (pl.grid > 0) {
     if (ws == nullptr || ws_bytes < workspace_of(pl, p)) return cudaErrorInvalidValue;
     a.part_o = static_cast<float*>(ws);
