@@ -724,7 +724,8 @@ template <int DV>
 __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) {
   __shared__ long long warp_sums[DV / 32];
   __shared__ long long s_before;
-  __shared__ float weight[DV];
+  __shared__ float2 weight[DV];   // and weighted sum
+  __shared__ float warp_max[DV / 32];
   const int row = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int heads = a.hc * a.G, hg = h / heads, hl = h % heads;
   const int per = (a.rows + DV - 1) / DV;
@@ -754,21 +755,29 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
   const float* ml = a.part_ml + (p0 * heads + hl) * 2;
   const float* po = a.part_o + (p0 * heads + hl) * DV + threadIdx.x;
   const size_t step = heads;
+  // the pieces' maximum
   float M = -INFINITY;
-  for (int p = 0; p < np; ++p) M = fmaxf(M, ml[p * step * 2]);
+  for (int p = threadIdx.x; p < np; p += DV) M = fmaxf(M, ml[p * step * 2]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < DV / 32; ++w) M = fmaxf(M, warp_max[w]);
   float L = 0.f, x = 0.f;
   for (int q = 0; q < np; q += DV) {
     const int nq = min(DV, np - q);
     __syncthreads();
     if ((int)threadIdx.x < nq) {
-      const float mp = ml[(q + threadIdx.x) * step * 2];
-      weight[threadIdx.x] = mp == -INFINITY ? 0.f : ex2_ftz(mp - M);
+      const float2 e = *reinterpret_cast<const float2*>(ml + (q + threadIdx.x) * step * 2);
+      const float w = e.x == -INFINITY ? 0.f : ex2_ftz(e.x - M);
+      weight[threadIdx.x] = make_float2(w, e.y * w);
     }
     __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
     for (int p = 0; p < nq; ++p) {
-      L = fmaf(ml[(q + p) * step * 2 + 1], weight[p], L);
-      x = fmaf(po[(q + p) * step * DV], weight[p], x);
+      L += weight[p].y;
+      x = fmaf(po[(q + p) * step * DV], weight[p].x, x);
     }
   }
   float f = L > 0.f ? a.c.v_scale / L : 0.f;
