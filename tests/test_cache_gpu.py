@@ -474,3 +474,123 @@ def test_window_attn_192_wide_and_no_first(lib, cuda_dev):
     f64 = lambda x: x.float().cpu().numpy().astype(np.float64)  # noqa: E731
     out = lib.dsa_window_attn(q, k, v, 100, n_first=20)
     check(out, *window_oracle(f64(q), f64(k), f64(v), 100, 20, None))
+
+
+# ----------------------------------------------------------------------------- further calls
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_more_rows_than_the_gpu_holds(lib, cuda_dev, fmt):
+    """Rows in plenty are taken whole, one CTA each; those without keys get zeros there too."""
+    s = Setup(lib, cuda_dev, fmt, B=3, ctx=90, page=16, HKV=2, DQK=64, DV=64)
+    pos = s.r.integers(-2, 90, (3, 250))
+    out = run_attn(s, pos, 2, window=20, n_first=2)
+    assert not out[torch.tensor(pos < 0, device=cuda_dev)].any()
+    idx = np.sort(s.r.integers(0, 90, (3, 250, 1)), -1)
+    run_attn(s, pos, 2, idx=idx)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_a_query_that_is_not_finite_stays_alone(lib, cuda_dev, fmt):
+    """An infinite or NaN query head gives NaN for itself, and nothing to the other heads and rows."""
+    s = Setup(lib, cuda_dev, fmt, B=2, ctx=70, page=16, HKV=2, DQK=64, DV=64)
+    q = s.cuda(s.normal(2, 2, 8, 64))
+    pos = torch.tensor([[69, 68], [30, 3]], dtype=torch.int32, device=cuda_dev)
+    clean = lib.dsa_cache_attn(q, s.cache, pos)
+    q[0, 1, 2, 5] = float("inf")
+    q[1, 0, 7, 0] = float("nan")
+    got = lib.dsa_cache_attn(q, s.cache, pos)
+    bad = torch.zeros(2, 2, 8, dtype=torch.bool, device=cuda_dev)
+    bad[0, 1, 2] = bad[1, 0, 7] = True
+    assert got[bad].isnan().all() and torch.equal(got[~bad], clean[~bad])
+
+
+def test_two_streams_at_once(lib, cuda_dev):
+    """Calls on two streams, each with its own workspace or outputs, at the same time."""
+    s = Setup(lib, cuda_dev, "e2m1", B=2, ctx=900, page=64, HKV=4, DQK=64, DV=64)
+    q = [s.cuda(s.normal(2, 1, 8, 64)) for _ in range(2)]
+    pos = torch.tensor([[899], [500]], dtype=torch.int32, device=cuda_dev)
+    want = [lib.dsa_cache_attn(x, s.cache, pos) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    need = int(lib.lib().dsa_cache_attn_workspace_bytes(s.cache.ref, 2, 1, 8, 0, 0))
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=cuda_dev)
+    got = [[], []]
+    for _ in range(20):
+        got[0].append(lib.dsa_cache_attn(q[0], s.cache, pos, stream=streams[0], ws=ws))
+        got[1].append(lib.dsa_cache_attn(q[1], s.cache, pos, stream=streams[1]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+    with pytest.raises(ValueError):
+        lib.dsa_cache_attn(q[0], s.cache, pos, ws=ws[: need - 1])
+
+
+def test_rows_past_four_gigabytes(lib, cuda_dev):
+    """Offsets in a large pool do not fit 32 bits: the last pages of 5.5 GB."""
+    HKV, DQK, DV, page, n_pages = 8, 192, 128, 64, 60000
+    pages = lib.dsa_cache_pages("e2m1", n_pages, page, HKV, DQK, DV, device=cuda_dev)
+    assert pages.numel() > 1 << 32
+    table = torch.tensor([[n_pages - 1, 3, n_pages - 2]], dtype=torch.int32, device=cuda_dev)
+    cache = lib.Cache(pages, table, HKV, DQK, DV)
+    small = Setup(lib, cuda_dev, "e2m1", B=1, ctx=192, page=page, HKV=HKV, DQK=DQK, DV=DV, fill=False)
+    g = torch.Generator(device=cuda_dev).manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device=cuda_dev).to(BF)  # noqa: E731
+    pos = torch.arange(192, dtype=torch.int32, device=cuda_dev)[None]
+    k, v, q = rand(1, 192, HKV, DQK), rand(1, 192, HKV, DV), rand(1, 192, 32, DQK)
+    for c in (cache, small.cache):
+        lib.dsa_cache_append(c, pos, k, v)
+    for x, y in zip(lib.dsa_cache_read(cache, pos), lib.dsa_cache_read(small.cache, pos)):
+        assert torch.equal(x, y)
+    last = pos[:, -3:].contiguous()
+    assert torch.equal(lib.dsa_cache_attn(q[:, -3:].contiguous(), cache, last),
+                       lib.dsa_cache_attn(q[:, -3:].contiguous(), small.cache, last))
+
+
+def test_rows_around_the_appended_ones_keep_their_bytes(lib, cuda_dev):
+    """Appending to one row of a page leaves the others, the pad bytes of its own among them."""
+    for fmt in ("bf16", "e2m1"):
+        s = Setup(lib, cuda_dev, fmt, B=1, ctx=32, page=8, HKV=1, DQK=64, DV=64, fill=False)
+        before = s.pages.view(torch.uint8).clone()
+        pos = torch.tensor([[9]], dtype=torch.int32, device=cuda_dev)
+        s.lib.dsa_cache_append(s.cache, pos, s.cuda(s.normal(1, 1, 1, 64)),
+                               s.cuda(s.normal(1, 1, 1, 64)))
+        changed = (s.pages.view(torch.uint8) != before).any(-1)
+        row = torch.zeros_like(changed)
+        row[s.table[0, 1], 1] = True
+        assert torch.equal(changed, row)
+        if fmt == "e2m1":
+            assert torch.equal(s.pages[..., 72:], before[..., 72:])
+
+
+def test_binding_refuses_what_does_not_fit(lib, cuda_dev):
+    s = Setup(lib, cuda_dev, "e2m1", B=2, ctx=32, page=8, HKV=2, DQK=64, DV=64)
+    pos = torch.zeros(2, 1, dtype=torch.int32, device=cuda_dev)
+    q, k = s.cuda(s.normal(2, 1, 4, 64)), s.cuda(s.normal(2, 1, 2, 64))
+    inv = torch.ones(16, device=cuda_dev)
+    bad = [
+        lambda: lib.dsa_cache_attn(q.float(), s.cache, pos),
+        lambda: lib.dsa_cache_attn(q[:1], s.cache, pos),
+        lambda: lib.dsa_cache_attn(q.cpu(), s.cache, pos),
+        lambda: lib.dsa_cache_attn(q.transpose(1, 2), s.cache, pos),
+        lambda: lib.dsa_cache_attn(q, s.cache, pos.long()),
+        lambda: lib.dsa_cache_attn(q, s.cache, pos[:1]),
+        lambda: lib.dsa_cache_attn(q, s.cache, pos, gate=q[..., 0, 0]),
+        lambda: lib.dsa_cache_attn(q, s.cache, pos, out=q.float()),
+        lambda: lib.dsa_cache_sparse_attn(q, s.cache, pos, pos.long()[..., None]),
+        lambda: lib.dsa_cache_append(s.cache, pos, k, q),
+        lambda: lib.dsa_cache_append(s.cache, pos, k, k, rope="half"),
+        lambda: lib.dsa_cache_append(s.cache, pos, k, k, q_out=q),
+        lambda: lib.dsa_cache_append(s.cache, pos, k, k, rope="half", inv_freq=inv, q_out=q),
+        lambda: lib.dsa_cache_append(s.cache, pos, k, k, rope="half", inv_freq=inv.double()),
+        lambda: lib.dsa_cache_read(s.cache, pos, k=q),
+        lambda: lib.Cache(s.pages, s.table.long(), 2, 64, 64),
+        lambda: lib.Cache(s.pages, s.table, 4, 64, 64),
+        lambda: lib.Cache(s.pages.float(), s.table, 2, 64, 64)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: lib.dsa_cache_attn(q, s.cache, pos, n_first=3),
+                 lambda: lib.dsa_cache_attn(q, s.cache, pos, window=-1),
+                 lambda: lib.dsa_cache_append(s.cache, pos, k, k, rope="half", inv_freq=inv[:8])):
+        with pytest.raises(lib.DSAError):
+            call()
