@@ -11,7 +11,8 @@
 // "前向流程": out *= act(gate[b,s,h]) in float32 before the cast.  [PANGU] §3.2: the SWA
 // layers use the same core with the band s+q_off-W < t <= s+q_off and grouped KV heads; where
 // the first tokens of the sequence stay visible (t < n_first <= 128), an item whose band starts
-// past key block 0 visits that block too, ahead of the band's.
+// past key block 0 visits that block too, ahead of the band's, with only the 16-key chunks that hold
+// first tokens (4096 tokens of 20 heads, window 512: 54 us, with 4 first tokens 59 us).
 //
 // Layout of one work item: Q block [128 x Dqk], K block [128 x Dqk] (both K-major bf16,
 // 128-byte swizzle, via 3-D tensor maps over (dim, head, token)), V block [128 x Dv]
@@ -82,10 +83,13 @@ struct AttnArgs {
   int band;              // item order: 0 = heads fastest, > 0 = bands of query blocks
 };
 
-template <int DQK_, int DV_, bool BAND_>
+// FIRST: the band form with visible first tokens (an instantiation of its own, so that the plain band
+// carries none of it: 3% of its time).
+template <int DQK_, int DV_, bool BAND_, bool FIRST_ = false>
 struct FaCfg {
   static constexpr int DQK = DQK_, DV = DV_;
-  static constexpr bool BAND = BAND_;
+  static constexpr bool BAND = BAND_, FIRST = FIRST_;
+  static_assert(BAND || !FIRST, "first tokens belong to the band");
   static constexpr int QKH = DQK / 64, VH = DV / 64;
   static constexpr int SLICE = kBlk * 128;          // one 64-element slice of a 128-row tile
   static constexpr int Q_BYTES = QKH * SLICE;
@@ -175,6 +179,9 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, const Item& it, int
   }
 }
 
+// Chunks of 16 keys that hold the first tokens.
+__device__ __forceinline__ int first_chunks(const AttnArgs& a) { return (a.n_first + 15) >> 4; }
+
 template <bool BAND>
 __device__ __forceinline__ int sink_blocks(const AttnArgs& a) {
   return a.nsink > 0 ? 1 : 0;
@@ -194,11 +201,12 @@ struct KeyBlocks {
   }
 };
 
+template <class C>
 __device__ __forceinline__ KeyBlocks key_blocks(const AttnArgs& a, const Item& it, int j0,
                                                 int j1) {
   KeyBlocks kb;
   kb.j0 = j0;
-  kb.lead = a.n_first > 0 && j0 > 0 ? 1 : 0;
+  kb.lead = C::FIRST && j0 > 0 ? 1 : 0;
   if (a.blist) {
     const size_t q = (size_t)it.b * a.nqb + it.qb;
     kb.list = a.blist + q * a.nkb;
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         const int kvh = it.h / group;
         const int sb = sink_blocks<C::BAND>(a);
-        const KeyBlocks kb = key_blocks(a, it, j0, j1);
+        const KeyBlocks kb = key_blocks<C>(a, it, j0, j1);
         const int nb = kb.n + sb;
         // key block of position r, read from the block list one position ahead
         int blk_next = nb > sb ? kb.at(0) : 0;
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // this thread issued before: one thread's tcgen05.mma instructions execute in issue
       // order, so those reads are done before this product writes the columns -- no wait
       // for P V_{g-2} to complete, and the tensor pipe never drains between blocks.
-      auto issue_qk = [&](uint32_t gg) -> bool {
+      auto issue_qk = [&](uint32_t gg, bool lead) -> bool {
         const int st = gg & 1;
         if (!mbar_wait(&k_full[st], (gg >> 1) & 1)) return false;
         tc_fence_after();
@@ -366,7 +374,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int kk = 0; kk < C::DQK / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::SLICE + (kk & 3) * 32;
           umma_f16_ss(tmem + (gg & 1) * C::S_COLS, qdesc0 + (uint64_t)(off >> 4),
-                      kd + (uint64_t)(off >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+                      kd + (uint64_t)(off >> 4),
+                      C::FIRST && lead ? idesc_bf16_f32(kBlk, 16 * first_chunks(a)) : idesc_qk,
+                      kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[gg & 1]);
         return true;
@@ -376,12 +386,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const Item it = item_of(a, i);
         int j0, j1;
         key_range<C::BAND>(a, it, &j0, &j1);
-        const int nb = key_blocks(a, it, j0, j1).n + sink_blocks<C::BAND>(a);
+        const KeyBlocks kb = key_blocks<C>(a, it, j0, j1);
+        const int sb = sink_blocks<C::BAND>(a), nb = kb.n + sb;
+        // the leading block of first tokens takes part with the chunks that hold any
+        auto is_lead = [&](int j) { return C::FIRST && kb.lead && j == sb; };
         if (!mbar_wait(q_full, ni & 1)) { ok = false; break; }
-        if (!issue_qk(g)) { ok = false; break; }
+        if (!issue_qk(g, is_lead(0))) { ok = false; break; }
         for (int j = 0; j < nb; ++j) {
           const uint32_t gg = g + j;
-          if (j + 1 < nb && !issue_qk(gg + 1)) { ok = false; break; }
+          if (j + 1 < nb && !issue_qk(gg + 1, is_lead(j + 1))) { ok = false; break; }
           if (j + 1 == nb) umma_commit(q_empty);  // Q free once the last S is computed
           if (!mbar_wait(&p_full[gg & 1], (gg >> 1) & 1)) { ok = false; break; }
           if (j == 0 && ni > 0 && !mbar_wait(o_empty, (ni - 1) & 1)) { ok = false; break; }
@@ -392,6 +405,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t o_tmem = tmem + C::O_COL + (C::BAND ? 0u : (gg & 1) * C::DV);
 #pragma unroll
           for (int kk = 0; kk < kBlk / 16; ++kk) {
+            if (C::FIRST && is_lead(j) && kk >= first_chunks(a)) break;
             // keys 16kk..16kk+15: 8 packed columns of P_hi at 16kk, P_lo 8 columns further;
             // V rows 16kk..: 2 swizzle atoms of 8 rows
             const uint32_t pc = 16 * kk;
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int j0, j1;
       key_range<C::BAND>(a, it, &j0, &j1);
       const int sb = sink_blocks<C::BAND>(a);
-      const KeyBlocks kb = key_blocks(a, it, j0, j1);
+      const KeyBlocks kb = key_blocks<C>(a, it, j0, j1);
       const int nb = kb.n + sb;
       const int s = it.qb * kBlk + row;
       const int spos = s + a.q_off;
@@ -442,7 +456,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       float m_used = ninf, l = 0.f;
       for (int j = 0; j < nb; ++j) {
         const uint32_t gg = g + j;
-        const int t0 = (j < sb ? 0 : kb.at(j - sb)) * kBlk + 64 * half;  // this half's first key
+        // the leading block of first tokens: the chunks of 16 keys that hold any, of this half's 4
+        const bool lead = C::FIRST && kb.lead && j == sb;
+        const int chunks = lead ? min(max(first_chunks(a) - 4 * half, 0), 4) : 4;
+        const int t0 = (C::FIRST ? (j < sb ? 0 : kb.at(j - sb)) : j0 + j - sb) * kBlk +
+                       64 * half;  // this half's first key
         uint32_t bits[2] = {0u, 0u};
         if (j < sb) {  // the sink block: its first nsink entries, visible to every query
 #pragma unroll
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // band: spos - window < t <= spos, t < T
           const int lo = max(spos - a.window + 1, 0) - t0, hi = min(spos, a.T - 1) - t0;
           // first tokens: t < n_first, t <= spos (key block 0 alone)
-          const int first = min(a.n_first - 1, hi + t0) - t0;
+          const int first = C::FIRST ? min(a.n_first - 1, hi + t0) - t0 : -1;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int a0 = max(lo - 32 * w, 0), a1 = min(hi - 32 * w, 31);
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                               : ((a1 - a0 == 31) ? 0xffffffffu
                                                  : (((1u << (a1 - a0 + 1)) - 1u) << a0));
             const int f1 = first - 32 * w;
-            if (f1 >= 0) bits[w] |= f1 >= 31 ? 0xffffffffu : (2u << f1) - 1u;
+            if (C::FIRST && f1 >= 0) bits[w] |= f1 >= 31 ? 0xffffffffu : (2u << f1) - 1u;
           }
         }
         if (!warp_wait(&s_full[gg & 1], (gg >> 1) & 1)) { ok = false; break; }
@@ -521,7 +539,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const unsigned long long nm2 = pack2(-m_used, -m_used);
           float mx[2] = {ninf, ninf};  // two chains
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) chunk(kk, nm2, mx[kk & 1]);
+          for (int kk = 0; kk < 4; ++kk)
+            if (!C::FIRST || kk < chunks) chunk(kk, nm2, mx[kk & 1]);
           mloc = fmaxf(mx[0], mx[1]);
         } else {
           float mx[4] = {ninf, ninf, ninf, ninf};
@@ -568,7 +587,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const unsigned long long nm2 = pack2(-msub, -msub);
           float mx = ninf;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) chunk(kk, nm2, mx);
+          for (int kk = 0; kk < 4; ++kk)
+            if (!C::FIRST || kk < chunks) chunk(kk, nm2, mx);
         }
         {
           float r0, r1;
@@ -661,7 +681,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int j0, j1;
       key_range<C::BAND>(a, it, &j0, &j1);
       const int sb = sink_blocks<C::BAND>(a);
-      const KeyBlocks kb = key_blocks(a, it, j0, j1);
+      const KeyBlocks kb = key_blocks<C>(a, it, j0, j1);
       const int nb = kb.n + sb;
       const int s = it.qb * kBlk + row;
       const int spos = s + a.q_off;
@@ -860,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const Item it = item_of(a, i);
       int j0, j1;
       key_range<C::BAND>(a, it, &j0, &j1);
-      const int nb = key_blocks(a, it, j0, j1).n + sink_blocks<C::BAND>(a);
+      const int nb = key_blocks<C>(a, it, j0, j1).n + sink_blocks<C::BAND>(a);
       const int s = it.qb * kBlk + row;
       const bool row_ok = s < a.S;
       // First the groups' (m, l): a group hands them over after publishing its last P, by
@@ -1071,7 +1091,7 @@ cudaError_t launch_fa(const AttnProblem& p, const uint32_t* mask, int mask_strid
   a.B = p.B; a.S = p.S; a.T = p.T; a.H = p.H; a.HKV = p.HKV; a.q_off = p.q_off;
   a.window = p.window; a.mask_stride = mask_stride;
   a.nsink = sinks ? p.nsink : 0;
-  a.n_first = C::BAND ? p.n_first : 0;
+  a.n_first = C::FIRST ? p.n_first : 0;
   if (a.n_first > kBlk) return cudaErrorNotSupported;  // one extra key block per item
   a.nqb = (p.S + kBlk - 1) / kBlk;
   a.bcount = bcount;
@@ -1124,11 +1144,14 @@ cudaError_t launch_masked_attn(const AttnProblem& p, const uint32_t* mask, int m
     bcount = cnt;
     blist = lst;
   }
+  const bool first = band && p.n_first > 0;
   if (p.DQK == 128)
-    return band ? launch_fa<FaCfg<128, 128, true>>(p, mask, mask_stride, bcount, blist, st)
-                : launch_fa<FaCfg<128, 128, false>>(p, mask, mask_stride, bcount, blist, st);
-  return band ? launch_fa<FaCfg<192, 128, true>>(p, mask, mask_stride, bcount, blist, st)
-              : launch_fa<FaCfg<192, 128, false>>(p, mask, mask_stride, bcount, blist, st);
+    return first ? launch_fa<FaCfg<128, 128, true, true>>(p, mask, mask_stride, bcount, blist, st)
+           : band ? launch_fa<FaCfg<128, 128, true>>(p, mask, mask_stride, bcount, blist, st)
+                  : launch_fa<FaCfg<128, 128, false>>(p, mask, mask_stride, bcount, blist, st);
+  return first ? launch_fa<FaCfg<192, 128, true, true>>(p, mask, mask_stride, bcount, blist, st)
+         : band ? launch_fa<FaCfg<192, 128, true>>(p, mask, mask_stride, bcount, blist, st)
+                : launch_fa<FaCfg<192, 128, false>>(p, mask, mask_stride, bcount, blist, st);
 }
 
 }  // namespace dsa
