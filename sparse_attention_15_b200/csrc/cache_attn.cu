@@ -170,7 +170,7 @@ struct Ring {
   // warps if that leaves two steps or more, else of 4.  (An SM has 228 KB, 1 KB of them for each
   // CTA's own use.)
   static constexpr int HALF = 113 * 1024, WHOLE = 226 * 1024;
-  static constexpr int WARPS = fits(2, 8) <= HALF ? 8 : 4;
+  static constexpr int WARPS = FMT == 1 ? 4 : fits(2, 8) <= HALF ? 8 : 4;
   static constexpr int STAGES = fits(3, WARPS) <= HALF ? 3 : 2;
   static constexpr int smem(int warps) {
     const int merge = warps * (16 + 8 * DV) * 4;
@@ -287,7 +287,7 @@ __device__ __forceinline__ void softmax_step(const float (&x)[4], float (&m)[2],
 }
 
 template <int FMT, int DQK, int DV>
-__global__ void __launch_bounds__(32 * kWarps, (Ring<FMT, DQK, DV>::WARPS == 8 ? 2 : 1))
+__global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::WARPS == 8 ? 2 : 1))
     cache_attn_kernel(const CacheAttnArgs a) {
   using S = Slot<FMT, DQK, DV>;
   using R = Ring<FMT, DQK, DV>;
@@ -827,7 +827,7 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   p->nw = nhw * p->kw;
   int smem = 0;
   with_dims(format, DQK, DV, [&](auto r) { smem = decltype(r)::smem(p->nw); });
-  const int resident = 148 * (smem <= 113 * 1024 ? 2 : 1);
+  const int resident = 148 * (format == 1 && p->nw <= 4 ? 4 : smem <= 113 * 1024 ? 2 : 1);
   // Pieces while they may fill the GPU better than the rows do: below two rounds of rows.  A piece
   // costs as much as some steps (its queries, the first copies' latency, its merge), so it has 8 of
   // them, or 4 where the rows leave more than half of the SMs idle (20 tokens with 16 steps in 5
