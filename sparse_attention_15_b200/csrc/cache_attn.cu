@@ -36,6 +36,7 @@
 // hi + lo, as one bf16 would be no more exact than the output.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "cache.cuh"
@@ -870,15 +871,31 @@ template <int FMT, int DQK, int DV>
 cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cudaStream_t st) {
   const int smem = Ring<FMT, DQK, DV>::smem(p.nw);
   auto kern = cache_attn_kernel<FMT, DQK, DV>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  // all of the SM's shared memory, or a second CTA would find too little of it
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
   const unsigned grid = p.grid > 0 ? (unsigned)p.grid : (unsigned)a.rows * (unsigned)p.nhg;
-  kern<<<grid, 32 * p.nw, smem, st>>>(a);
-  e = cudaGetLastError();
+  // The kernel's attributes are set once per device (each call of theirs costs a host microsecond),
+  // and again if a launch finds them gone, as after a device reset.
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ULL << dev : 0;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    const bool known = (ready.load(std::memory_order_relaxed) & bit) != 0 && attempt == 0;
+    if (!known) {
+      // the most that any call of this instantiation asks for
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Ring<FMT, DQK, DV>::smem(kWarps));
+      // all of the SM's shared memory, or a second CTA would find too little of it
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return e;
+      ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    kern<<<grid, 32 * p.nw, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (!known || e != cudaErrorInvalidValue) break;
+  }
   if (e != cudaSuccess || p.grid == 0) return e;
   // launched beside the pieces (programmatic dependence), so that its start costs no time after them
   cudaLaunchAttribute attr{};
