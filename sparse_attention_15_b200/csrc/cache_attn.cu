@@ -830,12 +830,14 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   with_dims(format, DQK, DV, [&](auto r) { smem = decltype(r)::smem(p->nw); });
   const int resident = 148 * (format == 1 && p->nw <= 4 ? 4 : smem <= 113 * 1024 ? 2 : 1);
   // Pieces while they may fill the GPU better than the rows do: below two rounds of rows.  A piece
-  // costs as much as some steps (its queries, the first copies' latency, its merge), so it has 8 of
-  // them, or 4 where the rows leave more than half of the SMs idle (20 tokens with 16 steps in 5
-  // groups: 21.5 us with 8, 30.7 us with 4; one token with 33 steps: 18.6 us and 16.5 us).
+  // costs as much as some steps (its queries, the first copies' latency, its part of the merge): the
+  // least piece has 8 steps, or 4 or 2 where that still leaves at most two CTAs, or one, per SM.  In
+  // us, for 2, 4 and 8 steps: one 4-bit window of 33 steps in 2 groups 11.7, 12.7, 16.6; 16 of them
+  // 18.0, 15.7, 17.5; one context of 257 steps 21.5, 15.7, 16.9; 20 tokens of 32 steps in 5 groups
+  // 23.0, 22.9, 19.1; 8 contexts of 257 steps 28.7, 28.7, 27.1.
   const long long ctas = (long long)rows * p->nhg;
-  p->least_log = ctas >= 74 ? 3 : 2;
   const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
+  p->least_log = steps <= 2 * 148 ? 1 : steps <= 8 * 148 ? 2 : 3;
   if (ctas < 2 * resident && (steps >> p->least_log) > ctas) {
     p->grid = (int)((steps >> p->least_log) < resident ? (steps >> p->least_log) : resident);
     // A cut inside a CTA's share costs a second piece, about kPiece steps: a grid that cuts rows of
