@@ -18,7 +18,9 @@
 // operation, so codes and scales are reproducible to the bit.  4 bits hold no infinity or NaN: a
 // group with one gets a NaN scale and reads back as NaN.
 //
-// Memory-bound: a thread takes a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's
+// Memory-bound in bf16 (8192 tokens of 32 heads, 520 MB: 90 us, 5.8 TB/s); in 4 bits (2 x 4001 tokens
+// of 8 heads, 246 MB: 62 us, 4.0 TB/s) latency and the encoding's instructions show.  A thread takes
+// a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's
 // maximum needs no exchange; a half-split thread takes both groups of its pairs.
 #include <float.h>
 #include <math.h>
