@@ -431,7 +431,8 @@ size_t dsa_cache_row_bytes(dsa_cache_format format, int HKV, int DQK, int DV);
  *
  *   rope_mode, rope_dim, inv_freq [rope_dim/2] float32: the last rope_dim dims of each key and
  *          query head are rotated by pos * inv_freq[j] ([DSV2] items 4-6: q/k heads are qk_nope +
- *          qk_rope wide), in float64, rounded to float32 and then to bf16.  rope_dim is a multiple
+ *          qk_rope wide).  The angle is float64, and a result what float64 rounded to float32 and
+ *          then to bf16 gives, but for about one in 2^30 (one bf16 step).  rope_dim is a multiple
  *          of 32, at most DQK.  DSA_ROPE_OFF: rope_dim 0, inv_freq NULL, and no q.
  *   q      [B,S,H,DQK] or NULL; q_out [B,S,H,DQK] out, may be q
  *   k_out  [B,S,HKV,DQK] out: the rotated keys as well, or NULL; may be k

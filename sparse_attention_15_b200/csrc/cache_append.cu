@@ -19,9 +19,9 @@
 // group with one gets a NaN scale and reads back as NaN.
 //
 // Memory-bound in bf16 (8192 tokens of 32 heads, 520 MB: 90 us, 5.8 TB/s); in 4 bits (2 x 4001 tokens
-// of 8 heads, 246 MB: 62 us, 4.0 TB/s) latency and the encoding's instructions show.  A thread takes
-// a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's
-// maximum needs no exchange; a half-split thread takes both groups of its pairs.
+// of 8 heads, 246 MB: 60 us, 4.1 TB/s) latency and the encoding's instructions show.  A thread takes
+// a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's maximum needs no exchange; a
+// half-split thread takes both groups of its pairs.
 #include <float.h>
 #include <math.h>
 
@@ -32,7 +32,12 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // of a CTA that reads
+// Threads of a CTA that appends: a CTA starts with its sines, which the other CTAs of its SM cover,
+// the better the more there are.  4-bit rows are smaller (2 x 4001 tokens of 8 heads, keys and
+// values only: 22 us by 128 threads, 28 by 256, 36 by 512); of 8192 bf16 tokens with queries the
+// rotated rows alone keep 256 busy (94 us; 128: 95, 512: 109).
+__host__ __device__ constexpr int append_threads(int format) { return format == 1 ? 128 : 256; }
 constexpr int kMaxTokens = 4;    // tokens per CTA
 
 // x / d for 0 <= x < 2^31, by a multiplier as in CacheView.
@@ -331,7 +336,9 @@ __device__ __forceinline__ int chunks_of(const Divisor& per_token, int nt) {
 }
 
 template <int FMT, int MODE>
-__global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(append_threads(FMT), 1024 / append_threads(FMT))
+    cache_append_kernel(const AppendArgs a) {
+  constexpr int kThreads = append_threads(FMT);
   extern __shared__ Turn turns[];  // [token][turn_at(J)]
   __shared__ uint8_t* row_of[kMaxTokens];
   __shared__ bool padding[kMaxTokens];
@@ -455,9 +462,10 @@ int tokens_per_cta(long long tokens, int format) {
 
 template <int FMT>
 void launch_append(const AppendArgs& a, int mode, unsigned grid, size_t smem, cudaStream_t st) {
-  if (mode == 0) cache_append_kernel<FMT, 0><<<grid, kThreads, smem, st>>>(a);
-  if (mode == 1) cache_append_kernel<FMT, 1><<<grid, kThreads, smem, st>>>(a);
-  if (mode == 2) cache_append_kernel<FMT, 2><<<grid, kThreads, smem, st>>>(a);
+  constexpr int threads = append_threads(FMT);
+  if (mode == 0) cache_append_kernel<FMT, 0><<<grid, threads, smem, st>>>(a);
+  if (mode == 1) cache_append_kernel<FMT, 1><<<grid, threads, smem, st>>>(a);
+  if (mode == 2) cache_append_kernel<FMT, 2><<<grid, threads, smem, st>>>(a);
 }
 
 }  // namespace
