@@ -463,7 +463,8 @@ dsa_status dsa_cache_read(const dsa_cache* cache, const int32_t* pos, int B, int
  *   query does not see are not read, whatever they hold.  A row without keys (padding, a context
  *   without pages) gets zeros.  Every visible key must have been appended.
  *   H <= 64.  Workspace (partial results of key slices) from dsa_cache_attn_workspace_bytes; 0 ->
- *   NULL is fine.
+ *   NULL is fine.  Its size depends on the shapes alone; calls that may run at the same time (on two
+ *   streams, or in two captured graphs) need a workspace each.
  */
 size_t dsa_cache_attn_workspace_bytes(const dsa_cache* cache, int B, int S, int H, int window,
                                       int n_first);

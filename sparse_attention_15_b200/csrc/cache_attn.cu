@@ -17,9 +17,9 @@
 // Work.  The (query token, group of KV heads) rows, laid end to end in steps of 16 keys, are cut
 // into equal pieces, one per resident CTA, whatever their lengths; a row in several pieces is
 // merged by a second kernel, in order.  Inside a CTA (of 4 warps for 4 bits, so that four fit an SM
-// and fewer wait for one) each warp works alone on one KV head (8 of
-// its query heads): it copies its own head's part of 16 keys at a time into its own ring
-// (cp.async, 16 bytes a lane, a step or two ahead), so the loop has no barrier and no producer.
+// and fewer wait for one) each warp works alone on one KV head (8 of its query heads): it copies its
+// own head's part of 16 keys at a time into its own ring (cp.async, 16 bytes a lane, a step or two
+// ahead), so the loop has no barrier and no producer.
 //
 // What bounds the 4-bit form: 9/16 byte a value, so at 6.5 TB/s 41 values arrive per clock and SM,
 // and each has to be widened to f16 before the tensor cores take it: about 22 instructions per 256
@@ -34,11 +34,11 @@
 // stay): half a step is 2^-11 each, below the rounding of the output.
 //
 // Measured: 64 x 2048 selected keys of 32 heads (755 MB) in 180 us, 4.2 TB/s; eight contexts of up to
-// 131072 tokens and 8 heads (1.13 GB) in 255-285 us, 4.0-4.4 TB/s.
+// 131072 tokens and 8 heads (1.13 GB) in 250-260 us, 4.4 TB/s.
 //
 // bf16 rows are bound by the bandwidth (16 x 2048 keys of 32 heads, 671 MB: 121 us, 5.5 TB/s).  They
-// are used as they are; probabilities are a bf16 pair
-// hi + lo, as one bf16 would be no more exact than the output.
+// are used as they are; probabilities are a bf16 pair hi + lo, as one bf16 would be no more exact than
+// the output.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -218,8 +218,8 @@ __device__ __forceinline__ int row_steps(const CacheAttnArgs& a, int row) {
 }
 
 // Pieces.  The steps of all rows (query tokens), once for each group of heads, are numbered end to
-// end, `each` for a group; CTA c of g takes numbers [c * all / g, (c + 1) * all / g).  Piece numbers
-// grow by one with each CTA and with each row: row r of group hg in CTA c is piece c + hg * R + r.
+// end, `each` for a group; share c of g has numbers [c * all / g, (c + 1) * all / g).  Piece numbers
+// grow by one with each CTA and with each row: row r of group hg in share c is piece c + hg * R + r.
 __device__ __forceinline__ int ctas_of(const CacheAttnArgs& a, long long all) {
   const long long most = all >> a.least_log;
   return (int)(most < 1 ? 1 : most < a.grid ? most : a.grid);
@@ -230,7 +230,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
-// The CTA that has step number s.
+// The share that has step number s.
 __device__ __forceinline__ int cta_of(long long s, long long all, int g) {
   return (int)quotient((s + 1) * g - 1, all);
 }
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long warp_sums[kWarps];
   __shared__ int first_row, first_step;
+  __shared__ uint32_t first_piece;  // the share's number: of its piece of row 0 in group 0
 
   // the merge kernel may start: it waits for this grid's end before it reads the pieces
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -333,9 +334,12 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
     const long long each = block_scan(mine, warp_sums, &before);
     const long long all = each * a.nhg;
     const int ctas = ctas_of(a, all);
-    if ((int)blockIdx.x >= ctas || all == 0) return;
-    const long long begin = quotient(blockIdx.x * all, ctas);
-    left = quotient((blockIdx.x + 1) * all, ctas) - begin;
+    // with groups of heads along x, neighbours read the same keys (make_plan says when)
+    const uint32_t share = blockIdx.x * gridDim.y + blockIdx.y;
+    if ((int)share >= ctas || all == 0) return;
+    const long long begin = quotient(share * all, ctas);
+    left = quotient((share + 1) * all, ctas) - begin;
+    if (threadIdx.x == 0) first_piece = share;
     hg = (int)quotient(begin, each);
     const long long in = begin - hg * each;
     if (before <= in && in < before + mine) {
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
     __syncthreads();
     // ---- merged over the key groups in order: the output row, or this piece of it
     const int heads = a.hc * a.G;
-    const size_t piece = (size_t)blockIdx.x + (size_t)hg * a.rows + row;
+    const size_t piece = (size_t)first_piece + (size_t)hg * a.rows + row;
     for (int i = threadIdx.x; i < heads * (DV / 4); i += blockDim.x) {
       const int hl = i / (DV / 4), d = (i % (DV / 4)) * 4;
       const int hh = hl % a.G;
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
 
 // How a call is laid out over CTAs.
 struct Plan {
-  int hc, nhg, nsub, kw, nw, grid, least_log;
+  int hc, nhg, nsub, kw, nw, grid, shares, least_log;
   size_t pieces;
 };
 
@@ -817,7 +821,8 @@ bool with_dims(int format, int DQK, int DV, F&& f) {
 constexpr int kPiece = 4;
 
 // Shapes only (no device query), so that workspace sizes are reproducible.
-bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long max_keys, Plan* p) {
+bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long max_keys,
+               bool selected, Plan* p) {
   *p = Plan{};
   p->nsub = (H / HKV + 7) / 8;
   int warps = 0;
@@ -852,6 +857,11 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
     const long long whole = ctas * (p->grid / ctas);
     if (whole > 0 && steps / whole + kPiece < steps / p->grid + 2 * kPiece) p->grid = (int)whole;
     p->pieces = (size_t)p->grid + (size_t)ctas;
+    // Rows are laid out by whole tokens, so two groups' parts of a row share 64-byte lines.  Read at
+    // the same time by neighbours, those come from memory once.  Eight contexts: 256 us, and 267 with
+    // each group's shares together; 64 windows: 43.5 and 44.4.  Selected keys gain nothing (64 x
+    // 2048: 184 us, 181).
+    if (!selected && p->least_log == 3 && p->grid % p->nhg == 0) p->shares = p->grid / p->nhg;
   }
   return true;
 }
@@ -872,14 +882,16 @@ size_t workspace_of(const Plan& pl, const CacheAttnProblem& p) {
 
 bool plan_of(const CacheAttnProblem& p, Plan* pl) {
   return make_plan(p.cache.format, p.B * p.S, p.H, p.cache.HKV, p.cache.DQK, p.cache.DV,
-                   max_keys_of(p), pl);
+                   max_keys_of(p), p.idx != nullptr, pl);
 }
 
 template <int FMT, int DQK, int DV>
 cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cudaStream_t st) {
   const int smem = Ring<FMT, DQK, DV>::smem(p.nw);
   auto kern = cache_attn_kernel<FMT, DQK, DV>;
-  const unsigned grid = p.grid > 0 ? (unsigned)p.grid : (unsigned)a.rows * (unsigned)p.nhg;
+  const dim3 grid = p.shares > 0 ? dim3((unsigned)p.nhg, (unsigned)p.shares)
+                    : p.grid > 0 ? dim3((unsigned)p.grid)
+                                 : dim3((unsigned)a.rows * (unsigned)p.nhg);
   // The kernel's attributes are set once per device (each call of theirs costs a host microsecond),
   // and again if a launch finds them gone, as after a device reset.
   static std::atomic<unsigned long long> ready{0};
@@ -922,7 +934,7 @@ cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cu
 
 bool cache_attn_supported(int format, int H, int HKV, int DQK, int DV) {
   Plan p;
-  return make_plan(format, 1, H, HKV, DQK, DV, 1, &p);
+  return make_plan(format, 1, H, HKV, DQK, DV, 1, false, &p);
 }
 
 size_t cache_attn_workspace_bytes(const CacheAttnProblem& p) {
