@@ -20,7 +20,8 @@ __all__ = [
     "dsa_sparse_attn_algo", "dsa_forward",
     "dsa_forward_workspace_bytes",
     "dsa_window_attn", "Cache", "dsa_cache_pages", "dsa_cache_row_bytes", "dsa_cache_append",
-    "dsa_cache_read", "dsa_cache_attn", "dsa_cache_sparse_attn", "dsa_sparse_attn_noalloc", "dsa_device_status", "dsa_version",
+    "dsa_cache_read", "dsa_cache_attn", "dsa_cache_sparse_attn", "dsa_sparse_attn_noalloc",
+    "dsa_device_status", "dsa_version",
     "dsa_test_arm_wait_timeout", "dsa_test_topk_bucket_floor", "LIB_PATH",
 ]
 
@@ -75,6 +76,7 @@ class CacheArgs(ctypes.Structure):
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_INT_MAX = 2 ** 31 - 1
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
 
@@ -456,7 +458,7 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
         out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
     if n_first:
         _check(lib().dsa_window_attn_first(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
-                                           int(n_first), _ptr(gate), gm, float(sm_scale),
+                                           min(int(n_first), _INT_MAX), _ptr(gate), gm, float(sm_scale),
                                            int(window), B, S, T, H, HKV, DQK, DV,
                                            ATTN_ALGO[algo], _ptr(out), _stream(stream)))
     elif sink_k is None:
@@ -605,12 +607,14 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
     else:
         op = takes("out", out, (B, S, H, cache.dv))
     L, c = lib(), cache.ref
+    # (past an int's range both see every key, as they do at its end)
+    window, n_first = min(int(window), _INT_MAX), min(int(n_first), _INT_MAX)
     K = 0 if idx is None else idx.shape[-1]
     ip = takes("idx", idx, (B, S, K), torch.int32)
     sizes = (B, S, H, K, window, n_first)
     nbytes = cache._workspaces.get(sizes)
     if nbytes is None:
-        nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, int(window), int(n_first))
+        nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, window, n_first)
                      if idx is None else L.dsa_cache_sparse_attn_workspace_bytes(c, B, S, H, K))
         cache._workspaces[sizes] = nbytes
     wp = None
@@ -626,8 +630,8 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
         wp = ws.data_ptr()
     st = _raw_stream(stream, cache.device)
     if idx is None:
-        _check(L.dsa_cache_attn(c, qp, pos.data_ptr(), int(window), int(n_first), gp, gm,
-                                float(sm_scale), B, S, H, op, wp, nbytes, st))
+        _check(L.dsa_cache_attn(c, qp, pos.data_ptr(), window, n_first, gp, gm, float(sm_scale), B, S,
+                                H, op, wp, nbytes, st))
     else:
         _check(L.dsa_cache_sparse_attn(c, qp, pos.data_ptr(), ip, K, gp, gm, float(sm_scale), B, S,
                                        H, op, wp, nbytes, st))

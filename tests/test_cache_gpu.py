@@ -322,6 +322,31 @@ def test_long_context_in_slices(lib, cuda_dev):
     run_attn(s, np.array([[2499], [700], [64]]), 4, window=640, n_first=33)
 
 
+@pytest.mark.parametrize("fmt,HKV", [("e2m1", 8), ("e2m1", 24), ("bf16", 16)])
+def test_groups_of_heads_side_by_side(lib, cuda_dev, fmt, HKV):
+    """Rows whose heads several CTAs share: every share of the grid at work, and a part of them."""
+    s = Setup(lib, cuda_dev, fmt, B=2, ctx=4807, page=64, HKV=HKV, DQK=64, DV=64)
+    for pos in ([[4806], [4790]], [[4000], [-1]], [[-1], [40]]):
+        run_attn(s, np.array(pos), HKV, gate=True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_windows_past_an_int(lib, cuda_dev, fmt):
+    """A window, or first tokens, of any size: past the context, every key."""
+    s = Setup(lib, cuda_dev, fmt, B=2, ctx=90, page=16, HKV=2, DQK=64, DV=64)
+    q = s.cuda(s.normal(2, 1, 4, 64))
+    pos = torch.tensor([[89], [30]], dtype=torch.int32, device=cuda_dev)
+    every = lib.dsa_cache_attn(q, s.cache, pos).float()
+    for window, n_first in ((90, 0), (2**31 - 1, 0), (2**32, 0), (2**40, 2**32), (1, 2**32), (3, 90)):
+        out = lib.dsa_cache_attn(q, s.cache, pos, window=window, n_first=n_first).float()
+        # two results for the same sums, each within the bound of it (sum p |v| <= max |v|)
+        bound = 2.0**-8 * torch.maximum(out.abs(), every.abs()) + 2.0**-10 * np.abs(s.v).max()
+        assert ((out - every).abs() <= 2 * bound).all()
+    kv = s.cuda(s.normal(1, 40, 2, 64))
+    with pytest.raises(lib.DSAError):
+        lib.dsa_window_attn(kv, kv, kv, 8, n_first=2**32)
+
+
 def test_same_result_every_time_and_out_given(lib, cuda_dev):
     s = Setup(lib, cuda_dev, "e2m1", B=4, ctx=700, page=64, HKV=4, DQK=64, DV=64)
     q = s.cuda(s.normal(4, 2, 8, 64))
