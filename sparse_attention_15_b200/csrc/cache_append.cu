@@ -454,7 +454,8 @@ TensorScale tensor_scale(float scale) {
 
 // Tokens per CTA: enough CTAs to fill the GPU first, then several tokens each (their sines in one
 // go, and their units spread over the warps): four 4-bit tokens (2 x 4001 tokens with reading back:
-// 79 us; two: 84 us; six: 98 us), two bf16 ones, whose rows are larger (8192: 149 us; four: 155 us).
+// 76 us; two: 81 us; three or six: 86-88 us), two bf16 ones, whose rows are larger (8192: 149 us;
+// four: 155 us).
 int tokens_per_cta(long long tokens, int format) {
   const long long per = tokens / (148 * 8), most = format == 1 ? 4 : 2;
   return (int)(per < 1 ? 1 : (per > most ? most : per));
