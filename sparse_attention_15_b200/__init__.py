@@ -1,9 +1,9 @@
 """Python binding of libdsa, the B200 DSA hot path (see include/dsa.h for the contract).
 
 Argument marshalling only: every function here reads sizes off torch tensors, allocates
-outputs (device memory plumbing) when the caller gives none, passes raw device pointers
-and the current CUDA stream to the C entry point of the same name, and raises DSAError
-on a non-OK status.  All compute runs in the library's CUDA kernels; there is no
+outputs and workspaces (device memory plumbing) when the caller gives none, passes raw device
+pointers and the CUDA stream (the current one, or the caller's `stream`) to the C entry point of
+the same name, and raises DSAError on a non-OK status.  All compute runs in the library's CUDA kernels; there is no
 fallback -- if libdsa.so is missing, importing a function raises.
 """
 from __future__ import annotations
@@ -163,6 +163,21 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _own(shape, dtype, device, stream, returned=True):
+    """A tensor that a call allocates for itself, from the pool of the stream it runs on.  (The pool
+    of another stream may hand out a block whose last use is still queued there.)  One that the
+    caller gets is kept from reuse until the current stream, too, is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dev(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -204,7 +219,7 @@ def dsa_index_scores(q_idx, k_idx, w, scale, relu="none", scores=None, stream=No
     B, S, HI, DI = q_idx.shape
     T = k_idx.shape[1]
     if scores is None:
-        scores = torch.empty((B, S, T), dtype=torch.float32, device=q_idx.device)
+        scores = _own((B, S, T), torch.float32, q_idx.device, stream)
     _check(lib().dsa_index_scores(_dtype_code(q_idx), _ptr(q_idx), _ptr(k_idx), _ptr(w),
                                   float(scale), RELU[relu], B, S, T, HI, DI, _ptr(scores),
                                   _stream(stream)))
@@ -219,9 +234,9 @@ def dsa_index_scores_collapsed(q_idx, k_idx, w, scale, relu="none", scores=None,
     B, S, HI, DI = q_idx.shape
     T = k_idx.shape[1]
     if scores is None:
-        scores = torch.empty((B, S, T), dtype=torch.float32, device=q_idx.device)
+        scores = _own((B, S, T), torch.float32, q_idx.device, stream)
     nbytes = int(lib().dsa_index_scores_collapsed_workspace_bytes(B, S, DI))
-    ws = _workspace(nbytes, q_idx.device, ws)
+    ws = _workspace(nbytes, q_idx.device, ws, stream)
     _check(lib().dsa_index_scores_collapsed(_dtype_code(q_idx), _ptr(q_idx), _ptr(k_idx), _ptr(w),
                                             float(scale), RELU[relu], B, S, T, HI, DI,
                                             _ptr(scores), _ptr(ws), nbytes, _stream(stream)))
@@ -233,7 +248,7 @@ def dsa_hadamard_rotate(x, out=None, stream=None):
     _dev(x, out)
     d = x.shape[-1]
     if out is None:
-        out = torch.empty_like(x)
+        out = _own(x.shape, x.dtype, x.device, stream)
     _check(lib().dsa_hadamard_rotate(_dtype_code(x), _ptr(x), x.numel() // d, d, _ptr(out),
                                      _stream(stream)))
     return out
@@ -244,7 +259,7 @@ def dsa_topk(scores, K, idx=None, stream=None):
     _dev(scores, idx)
     B, S, T = scores.shape
     if idx is None:
-        idx = torch.empty((B, S, K), dtype=torch.int32, device=scores.device)
+        idx = _own((B, S, K), torch.int32, scores.device, stream)
     _check(lib().dsa_topk(_ptr(scores), B, S, T, int(K), _ptr(idx), _stream(stream)))
     return idx
 
@@ -264,9 +279,9 @@ def dsa_index_topk(q_idx, k_idx, w, scale, K, relu="none", idx=None, ws=None,
     T = k_idx.shape[1]
     k_eff = min(int(K), T)
     if idx is None:
-        idx = torch.empty((B, S, k_eff), dtype=torch.int32, device=q_idx.device)
+        idx = _own((B, S, k_eff), torch.int32, q_idx.device, stream)
     nbytes = dsa_index_topk_workspace_bytes(B, S, T, int(K))
-    ws = _workspace(nbytes, q_idx.device, ws)
+    ws = _workspace(nbytes, q_idx.device, ws, stream)
     _check(lib().dsa_index_topk(_dtype_code(q_idx), _ptr(q_idx), _ptr(k_idx), _ptr(w),
                                 float(scale), RELU[relu], B, S, T, HI, DI, int(K), _ptr(idx),
                                 _ptr(ws), nbytes, _ptr(fallback_out), _stream(stream)))
@@ -285,11 +300,11 @@ def dsa_sparse_attn_algo(dtype, B, S, T, H, DQK, DV, K, algo="auto") -> str:
     return {v: k for k, v in ATTN_ALGO.items()}[r]
 
 
-def _workspace(nbytes, device, ws):
+def _workspace(nbytes, device, ws, stream):
     if nbytes == 0:
         return ws
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = _own(nbytes, torch.uint8, device, stream, returned=False)
     return ws
 
 
@@ -303,9 +318,9 @@ def dsa_sparse_attn(q, k, v, idx, gate=None, gate_mode=None, sm_scale=0.0, algo=
     K = idx.shape[-1]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
-        out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
+        out = _own((B, S, H, DV), q.dtype, q.device, stream)
     nbytes = dsa_sparse_attn_workspace_bytes(_dtype_code(q), B, S, T, H, DQK, DV, K, algo)
-    ws = _workspace(nbytes, q.device, ws)
+    ws = _workspace(nbytes, q.device, ws, stream)
     _check(lib().dsa_sparse_attn(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), K,
                                  _ptr(gate), gm, float(sm_scale), B, S, T, H, DQK, DV,
                                  ATTN_ALGO[algo], _ptr(out), _ptr(ws), nbytes, _stream(stream)))
@@ -323,10 +338,10 @@ def dsa_sparse_attn_sinks(q, k, v, idx, sink_k, sink_v, gate=None, gate_mode=Non
     NS = sink_k.shape[0]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
-        out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
+        out = _own((B, S, H, DV), q.dtype, q.device, stream)
     nbytes = int(lib().dsa_sparse_attn_sinks_workspace_bytes(_dtype_code(q), B, S, T, H, DQK, DV,
                                                              K, NS, ATTN_ALGO[algo]))
-    ws = _workspace(nbytes, q.device, ws)
+    ws = _workspace(nbytes, q.device, ws, stream)
     _check(lib().dsa_sparse_attn_sinks(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), K,
                                        _ptr(sink_k), _ptr(sink_v), NS, _ptr(gate), gm,
                                        float(sm_scale), B, S, T, H, DQK, DV, ATTN_ALGO[algo],
@@ -345,7 +360,7 @@ def dsa_sparse_attn_noalloc(q, k, v, idx, gate=None, gate_mode=None, sm_scale=0.
     K = idx.shape[-1]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
-        out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
+        out = _own((B, S, H, DV), q.dtype, q.device, stream)
     _check(lib().dsa_sparse_attn_noalloc(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(idx), K,
                                          _ptr(gate), gm, float(sm_scale), B, S, T, H, DQK, DV,
                                          _ptr(out), _stream(stream)))
@@ -364,9 +379,9 @@ def dsa_sparse_attn_latent(q, kv, idx, dv=512, sink_kv=None, gate=None, gate_mod
     NS = 0 if sink_kv is None else int(sink_kv.shape[0])
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
-        out = torch.empty((B, S, H, dv), dtype=q.dtype, device=q.device)
+        out = _own((B, S, H, dv), q.dtype, q.device, stream)
     nbytes = int(lib().dsa_sparse_attn_latent_workspace_bytes(B, S, H, K, NS))
-    ws = _workspace(nbytes, q.device, ws)
+    ws = _workspace(nbytes, q.device, ws, stream)
     _check(lib().dsa_sparse_attn_latent(_dtype_code(q), _ptr(q), _ptr(kv), _ptr(idx), K,
                                         _ptr(sink_kv), NS, _ptr(gate), gm, float(sm_scale), B, S,
                                         T, H, DQK, int(dv), _ptr(out), _ptr(ws), nbytes,
@@ -423,10 +438,10 @@ def dsa_forward(q_idx, k_idx, w, index_scale, K, q, k, v, gate=None, gate_mode=N
     T = k_idx.shape[1]
     if out is None:
         DV = int(dv) if attn_form == "latent" else v.shape[-1]
-        out = torch.empty((B, S, q.shape[2], DV), dtype=q.dtype, device=q.device)
+        out = _own((B, S, q.shape[2], DV), q.dtype, q.device, stream)
     k_eff = min(int(K), T)
     if idx_out is None:
-        idx_out = torch.empty((B, S, k_eff), dtype=torch.int32, device=q.device)
+        idx_out = _own((B, S, k_eff), torch.int32, q.device, stream)
     a = _forward_args(q_idx, k_idx, w, index_scale, K, q, k, v, gate, gate_mode, relu, sm_scale,
                       attn_algo, out, scores_out, idx_out, indexer, sink_k, sink_v, attn_form,
                       dv, topk_fallback_out)
@@ -438,7 +453,7 @@ def dsa_forward(q_idx, k_idx, w, index_scale, K, q, k, v, gate=None, gate_mode=N
         ev_arr = (ctypes.c_void_p * 4)(*[e.cuda_event for e in events])
         a.events = ctypes.cast(ev_arr, ctypes.c_void_p).value
     nbytes = dsa_forward_workspace_bytes(a) if ws_bytes is None else int(ws_bytes)
-    ws = _workspace(nbytes, q.device, ws)
+    ws = _workspace(nbytes, q.device, ws, stream)
     _check(lib().dsa_forward(ctypes.byref(a), _ptr(ws), nbytes, _stream(stream)))
     return out, idx_out
 
@@ -455,7 +470,7 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
     T, HKV, DV = k.shape[1], k.shape[2], v.shape[-1]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     if out is None:
-        out = torch.empty((B, S, H, DV), dtype=q.dtype, device=q.device)
+        out = _own((B, S, H, DV), q.dtype, q.device, stream)
     if n_first:
         _check(lib().dsa_window_attn_first(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
                                            min(int(n_first), _INT_MAX), _ptr(gate), gm, float(sm_scale),
@@ -528,6 +543,11 @@ class Cache:
         self._takes("pos", pos, pos.shape, torch.int32)
         return pos.shape
 
+    def _output(self, shape, stream):
+        """A call's bf16 output (new_empty is the cheaper call, by 1 us)."""
+        return self._bf16.new_empty(shape) if stream is None else \
+            _own(shape, torch.bfloat16, self.device, stream)
+
     def _takes(self, name, t, shape, dtype=torch.bfloat16):
         """A call's tensor: contiguous, of this shape and type, on the cache's device; its address
         (None: not given)."""
@@ -571,7 +591,7 @@ def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=
             qs = (B, S, H, cache.dqk)
             qp = takes("q", q, qs)
             if q_out is None:
-                q_out = torch.empty_like(q)
+                q_out = _own(qs, q.dtype, q.device, stream)
             qo = takes("q_out", q_out, qs)
         elif q_out is not None:
             raise ValueError("q_out goes with q")
@@ -586,9 +606,9 @@ def dsa_cache_read(cache, pos, k=None, v=None, stream=None):
     B, S = cache._rows(pos)
     ks, vs = (B, S, cache.kv_heads, cache.dqk), (B, S, cache.kv_heads, cache.dv)
     if k is None:
-        k = cache._bf16.new_empty(ks)
+        k = cache._output(ks, stream)
     if v is None:
-        v = cache._bf16.new_empty(vs)
+        v = cache._output(vs, stream)
     _check(lib().dsa_cache_read(cache.ref, pos.data_ptr(), B, S, cache._takes("k", k, ks),
                                 cache._takes("v", v, vs), _raw_stream(stream, cache.device)))
     return k, v
@@ -602,7 +622,7 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
     qp = takes("q", q, (B, S, H, cache.dqk))
     gp = takes("gate", gate, (B, S, H))
     if out is None:
-        out = cache._bf16.new_empty((B, S, H, cache.dv))
+        out = cache._output((B, S, H, cache.dv), stream)
         op = out.data_ptr()
     else:
         op = takes("out", out, (B, S, H, cache.dv))
@@ -620,9 +640,7 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
     wp = None
     if nbytes:
         if ws is None:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-            if stream is not None:
-                ws.record_stream(stream)  # not to be handed out again before that stream is done
+            ws = _own(nbytes, torch.uint8, cache.device, stream, returned=False)
         elif not ws.is_contiguous() or ws.device != cache.device or \
                 ws.numel() * ws.element_size() < nbytes:
             raise ValueError(f"ws is a contiguous tensor of at least {nbytes} bytes on "

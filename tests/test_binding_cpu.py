@@ -1,0 +1,127 @@
+"""The Python binding without a GPU: a library that only answers, CPU tensors in the place of device
+memory, and what the binding allocates and passes looked at."""
+import contextlib
+
+import pytest
+import torch
+
+import sparse_attention_15_b200 as dsa
+
+BF = torch.bfloat16
+
+
+class Answers:
+    """Every entry point succeeds and is recorded; workspaces have 4096 bytes, cache rows their size."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            if name == "dsa_cache_row_bytes":
+                fmt, kv, dqk, dv = args
+                n = kv * (dqk + dv)
+                return 2 * n if fmt == 0 else (n // 2 + n // 16 + 15) // 16 * 16
+            return 4096 if name.endswith("workspace_bytes") else 0
+
+        return call
+
+    def last(self, name):
+        return next(args for n, args in reversed(self.calls) if n == name)
+
+
+class Stream:
+    """Stands for a CUDA stream of the caller."""
+    cuda_stream = 0x5000
+
+
+class Current:
+    cuda_stream = 0
+
+
+@pytest.fixture
+def answers(monkeypatch):
+    """The binding on CPU tensors; `.made` lists (shape, dtype, inside the side stream's context) of
+    each tensor that it makes, `.recorded` those kept for the current stream."""
+    a = Answers()
+    a.made, a.recorded, a.inside = [], [], False
+    empty = torch.empty
+
+    def made(*args, **kw):
+        t = empty(*args, **kw)
+        a.made.append((t, a.inside))
+        return t
+
+    @contextlib.contextmanager
+    def on(stream):
+        assert stream is Stream
+        a.inside = True
+        yield
+        a.inside = False
+
+    monkeypatch.setattr(dsa, "_LIB", a)
+    monkeypatch.setattr(dsa, "_dev", lambda *ts: None)
+    monkeypatch.setattr(torch, "empty", made)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Current)
+    monkeypatch.setattr(dsa, "_raw_stream", lambda stream, device: (stream or Current).cuda_stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: a.recorded.append((t, s)))
+    return a
+
+
+def some_cache(fmt="e2m1", B=2, kv=2, D=64):
+    return dsa.Cache(dsa.dsa_cache_pages(fmt, 8, 16, kv, D, D, device="cpu"),
+                     torch.zeros(B, 4, dtype=torch.int32), kv, D, D)
+
+
+def calls():
+    """Each call that allocates, all of its outputs and workspace left to it."""
+    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    i32 = torch.int32
+    qi, ki, w = z(2, 1, 4, 64), z(2, 32, 64), z(2, 1, 4, dtype=torch.float32)
+    q, k = z(2, 1, 4, 64), z(2, 32, 4, 64)
+    idx, pos = z(2, 1, 8, dtype=i32), z(2, 1, dtype=i32)
+    kv, new = z(2, 32, 576), z(2, 1, 2, 64)
+    c = some_cache()
+    inv = torch.ones(16)
+    return [
+        (dsa.dsa_index_scores, (qi, ki, w, 1.0), {}),
+        (dsa.dsa_index_scores_collapsed, (qi, ki, w, 1.0), {}),
+        (dsa.dsa_hadamard_rotate, (qi,), {}),
+        (dsa.dsa_topk, (z(2, 1, 32, dtype=torch.float32), 8), {}),
+        (dsa.dsa_index_topk, (qi, ki, w, 1.0, 8), {}),
+        (dsa.dsa_sparse_attn, (q, k, k, idx), {}),
+        (dsa.dsa_sparse_attn_sinks, (q, k, k, idx, z(3, 4, 64), z(3, 4, 64)), {}),
+        (dsa.dsa_sparse_attn_noalloc, (q, k, k, idx), {}),
+        (dsa.dsa_sparse_attn_latent, (z(2, 1, 4, 576), kv, idx), {}),
+        (dsa.dsa_forward, (qi, ki, w, 1.0, 8, q, k, k), {}),
+        (dsa.dsa_window_attn, (q, k, k, 8), {}),
+        (dsa.dsa_window_attn, (q, k, k, 8), dict(n_first=4)),
+        (dsa.dsa_cache_append, (c, pos, new, new), dict(rope="half", inv_freq=inv, q=q)),
+        (dsa.dsa_cache_read, (c, pos), {}),
+        (dsa.dsa_cache_attn, (q, c, pos), {}),
+        (dsa.dsa_cache_sparse_attn, (q, c, pos, idx), {}),
+    ]
+
+
+@pytest.mark.parametrize("n", range(16))
+def test_a_call_on_another_stream_allocates_there(answers, n):
+    """A block of the current stream's pool may still be in use there, so outputs and workspaces of a
+    call on another stream come from that stream's own; outputs are kept for the current one."""
+    fn, args, kw = calls()[n]
+    answers.made.clear()
+    out = fn(*args, stream=Stream(), **kw)
+    assert answers.made and all(inside for _, inside in answers.made), fn.__name__
+    out = [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+    assert [t.data_ptr() for t, s in answers.recorded if s is Current] == \
+        [t.data_ptr() for t, _ in answers.made if any(t is o for o in out)]
+    assert len(answers.recorded) == len(out)
+
+
+def test_calls_on_the_current_stream_allocate_plainly(answers):
+    for fn, args, kw in calls():
+        fn(*args, **kw)
+    assert not answers.recorded and not any(inside for _, inside in answers.made)
