@@ -178,6 +178,12 @@ def _own(shape, dtype, device, stream, returned=True):
     return t
 
 
+def _int(x):
+    """An argument as a C int: past its range the end of the range (ctypes would wrap it), which the
+    library refuses, or takes as a window or a number of keys that covers every key."""
+    return max(-_INT_MAX - 1, min(int(x), _INT_MAX))
+
+
 def _dev(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -260,13 +266,13 @@ def dsa_topk(scores, K, idx=None, stream=None):
     B, S, T = scores.shape
     if idx is None:
         idx = _own((B, S, K), torch.int32, scores.device, stream)
-    _check(lib().dsa_topk(_ptr(scores), B, S, T, int(K), _ptr(idx), _stream(stream)))
+    _check(lib().dsa_topk(_ptr(scores), B, S, T, _int(K), _ptr(idx), _stream(stream)))
     return idx
 
 
 
 def dsa_index_topk_workspace_bytes(B, S, T, K) -> int:
-    return int(lib().dsa_index_topk_workspace_bytes(B, S, T, K))
+    return int(lib().dsa_index_topk_workspace_bytes(B, S, T, _int(K)))
 
 
 def dsa_index_topk(q_idx, k_idx, w, scale, K, relu="none", idx=None, ws=None,
@@ -280,10 +286,10 @@ def dsa_index_topk(q_idx, k_idx, w, scale, K, relu="none", idx=None, ws=None,
     k_eff = min(int(K), T)
     if idx is None:
         idx = _own((B, S, k_eff), torch.int32, q_idx.device, stream)
-    nbytes = dsa_index_topk_workspace_bytes(B, S, T, int(K))
+    nbytes = dsa_index_topk_workspace_bytes(B, S, T, K)
     ws = _workspace(nbytes, q_idx.device, ws, stream)
     _check(lib().dsa_index_topk(_dtype_code(q_idx), _ptr(q_idx), _ptr(k_idx), _ptr(w),
-                                float(scale), RELU[relu], B, S, T, HI, DI, int(K), _ptr(idx),
+                                float(scale), RELU[relu], B, S, T, HI, DI, _int(K), _ptr(idx),
                                 _ptr(ws), nbytes, _ptr(fallback_out), _stream(stream)))
     return idx
 
@@ -399,7 +405,7 @@ def _forward_args(q_idx, k_idx, w, index_scale, K, q, k, v, gate, gate_mode, rel
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
     a = ForwardArgs(
         dtype=_dtype_code(q), B=B, S=S, T=T, HI=HI, DI=DI, index_scale=float(index_scale),
-        relu=RELU[relu], K=int(K), H=H, DQK=DQK, DV=DV, sm_scale=float(sm_scale), gate_mode=gm,
+        relu=RELU[relu], K=_int(K), H=H, DQK=DQK, DV=DV, sm_scale=float(sm_scale), gate_mode=gm,
         attn_algo=ATTN_ALGO[attn_algo], q_idx=q_idx.data_ptr(), k_idx=k_idx.data_ptr(),
         w=w.data_ptr(), q=q.data_ptr(), k=k.data_ptr(), v=None if v is None else v.data_ptr(),
         gate=None if gate is None else gate.data_ptr(), out=out.data_ptr(),
@@ -464,6 +470,7 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
     optional attention sinks sink_k [NS,HKV,DQK], sink_v [NS,HKV,DV] (NS <= 128), or the
     sequence's first n_first tokens (<= 128) staying visible."""
     _dev(q, k, v, gate, out, sink_k, sink_v)
+    window, n_first = _int(window), _int(n_first)
     if n_first and sink_k is not None:
         raise ValueError("sink_k / sink_v and n_first are alternatives")
     B, S, H, DQK = q.shape
@@ -473,17 +480,17 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
         out = _own((B, S, H, DV), q.dtype, q.device, stream)
     if n_first:
         _check(lib().dsa_window_attn_first(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
-                                           min(int(n_first), _INT_MAX), _ptr(gate), gm, float(sm_scale),
-                                           int(window), B, S, T, H, HKV, DQK, DV,
+                                           n_first, _ptr(gate), gm, float(sm_scale), window, B,
+                                           S, T, H, HKV, DQK, DV,
                                            ATTN_ALGO[algo], _ptr(out), _stream(stream)))
     elif sink_k is None:
         _check(lib().dsa_window_attn(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), gm,
-                                     float(sm_scale), int(window), B, S, T, H, HKV, DQK, DV,
+                                     float(sm_scale), window, B, S, T, H, HKV, DQK, DV,
                                      ATTN_ALGO[algo], _ptr(out), _stream(stream)))
     else:
         _check(lib().dsa_window_attn_sinks(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
                                            _ptr(sink_k), _ptr(sink_v), int(sink_k.shape[0]),
-                                           _ptr(gate), gm, float(sm_scale), int(window), B, S,
+                                           _ptr(gate), gm, float(sm_scale), window, B, S,
                                            T, H, HKV, DQK, DV, ATTN_ALGO[algo], _ptr(out),
                                            _stream(stream)))
     return out
@@ -492,7 +499,7 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
 # --------------------------------------------------------------------------- paged cache
 def dsa_cache_row_bytes(fmt, kv_heads, dqk, dv) -> int:
     """Bytes of one token's row; fmt "bf16" or "e2m1" (4 bits)."""
-    return int(lib().dsa_cache_row_bytes(CACHE_FORMAT[fmt], kv_heads, dqk, dv))
+    return int(lib().dsa_cache_row_bytes(CACHE_FORMAT[fmt], _int(kv_heads), _int(dqk), _int(dv)))
 
 
 def dsa_cache_pages(fmt, n_pages, page_size, kv_heads, dqk, dv, device="cuda"):
@@ -525,8 +532,8 @@ class Cache:
             raise ValueError("pages and table are on different devices")
         self.pages, self.table, self.device = pages, table, pages.device
         self.kv_heads, self.dqk, self.dv = int(kv_heads), int(dqk), int(dv)
-        self.args = CacheArgs(format=CACHE_FORMAT[fmt], n_pages=pages.shape[0],
-                              page_size=pages.shape[1], max_pages=table.shape[1],
+        self.args = CacheArgs(format=CACHE_FORMAT[fmt], n_pages=_int(pages.shape[0]),
+                              page_size=_int(pages.shape[1]), max_pages=_int(table.shape[1]),
                               HKV=self.kv_heads, DQK=self.dqk, DV=self.dv,
                               k_scale=float(k_scale), v_scale=float(v_scale),
                               pages=pages.data_ptr(), table=table.data_ptr())
@@ -627,8 +634,7 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
     else:
         op = takes("out", out, (B, S, H, cache.dv))
     L, c = lib(), cache.ref
-    # (past an int's range both see every key, as they do at its end)
-    window, n_first = min(int(window), _INT_MAX), min(int(n_first), _INT_MAX)
+    window, n_first = _int(window), _int(n_first)
     K = 0 if idx is None else idx.shape[-1]
     ip = takes("idx", idx, (B, S, K), torch.int32)
     sizes = (B, S, H, K, window, n_first)

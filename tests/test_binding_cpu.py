@@ -125,3 +125,45 @@ def test_calls_on_the_current_stream_allocate_plainly(answers):
     for fn, args, kw in calls():
         fn(*args, **kw)
     assert not answers.recorded and not any(inside for _, inside in answers.made)
+
+
+# ----------------------------------------------------------------------------- sizes past an int
+TOP = 2**31 - 1
+
+
+@pytest.mark.parametrize("given,passed", [(8, 8), (TOP, TOP), (2**31, TOP), (2**32, TOP),
+                                          (2**32 + 8, TOP), (2**40, TOP), (-1, -1),
+                                          (-2**32, -TOP - 1), (-2**32 + 8, -TOP - 1)])
+def test_sizes_past_an_int_do_not_wrap(answers, given, passed):
+    """What a C int does not hold arrives as its last value on that side."""
+    q, k, sink = torch.zeros(2, 1, 4, 64, dtype=BF), torch.zeros(2, 32, 4, 64, dtype=BF), \
+        torch.zeros(3, 4, 64, dtype=BF)
+    c, pos = some_cache(), torch.zeros(2, 1, dtype=torch.int32)
+    qi, ki, w = q[:, :, :, :64], torch.zeros(2, 32, 64, dtype=BF), torch.zeros(2, 1, 4)
+    dsa.dsa_window_attn(q, k, k, given)
+    assert answers.last("dsa_window_attn")[7] == passed
+    dsa.dsa_window_attn(q, k, k, given, sink_k=sink, sink_v=sink)
+    assert answers.last("dsa_window_attn_sinks")[10] == passed
+    dsa.dsa_window_attn(q, k, k, given, n_first=given)
+    args = answers.last("dsa_window_attn_first")
+    assert (args[4], args[8]) == (passed, passed)
+    dsa.dsa_cache_attn(q, c, pos, window=given, n_first=given)
+    assert answers.last("dsa_cache_attn_workspace_bytes")[4:] == (passed, passed)
+    assert answers.last("dsa_cache_attn")[3:5] == (passed, passed)
+    if given > 0:
+        idx = torch.zeros(2, 1, 32, dtype=torch.int32)
+        dsa.dsa_index_topk(qi, ki, w, 1.0, given, idx=idx)
+        assert answers.last("dsa_index_topk")[11] == passed
+        assert answers.last("dsa_index_topk_workspace_bytes")[3] == passed
+        dsa.dsa_forward(qi, ki, w, 1.0, given, q, k, k, idx_out=idx)
+        assert answers.last("dsa_forward")[0]._obj.K == passed
+
+
+def test_a_window_past_an_int_is_refused_or_sees_every_key(lib):
+    """The library's part: a window of any positive size is taken, a negative one is not."""
+    L, FAKE = lib.lib(), 0x10000
+    for window in (-TOP - 1, -1, 0):
+        assert L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, 4, None, 0, 0.0, window, 1, 64, 64, 4, 2,
+                                       128, 128, 0, FAKE, None) == 1
+    assert L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, -TOP - 1, None, 0, 0.0, 8, 1, 64, 64, 4, 2,
+                                   128, 128, 0, FAKE, None) == 1

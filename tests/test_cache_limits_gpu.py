@@ -49,3 +49,32 @@ def test_a_side_stream_takes_no_block_of_the_current_one(lib, cuda_dev):
     outs += [lib.dsa_window_attn(q, q, q, 1, stream=side)]
     assert not at & {t.data_ptr() for t in outs}
     torch.cuda.synchronize()
+
+
+# ----------------------------------------------------------------------------- sizes past an int
+@pytest.mark.parametrize("dtype,D,S", [(BF, 128, 70), (BF, 64, 70), (torch.float32, 64, 9)])
+def test_contiguous_windows_past_an_int(lib, cuda_dev, dtype, D, S):
+    """A window of any size past the context is the window of the whole context; one below the range
+    of an int is as negative as any other."""
+    g = torch.Generator(device=cuda_dev).manual_seed(D + S)
+    rand = lambda *sh: torch.randn(*sh, generator=g, device=cuda_dev).to(dtype)  # noqa: E731
+    q, k, v = rand(2, S, 4, D), rand(2, 90, 2, D), rand(2, 90, 2, D)
+    sink_k, sink_v = rand(3, 2, D), rand(3, 2, D)
+    for kw in (dict(), dict(n_first=5), dict(sink_k=sink_k, sink_v=sink_v)):
+        every = lib.dsa_window_attn(q, k, v, 90, **kw)
+        for window in (2**31 - 1, 2**32, 2**32 + 8, 2**40):
+            assert torch.equal(lib.dsa_window_attn(q, k, v, window, **kw), every)
+        for window in (-2**32, -2**32 + 8):
+            with pytest.raises(lib.DSAError):
+                lib.dsa_window_attn(q, k, v, window, **kw)
+    for n_first in (-2**32, -2**32 + 8):
+        with pytest.raises(lib.DSAError):
+            lib.dsa_window_attn(q, k, v, 8, n_first=n_first)
+
+
+def test_cache_windows_below_an_int_are_refused(lib, cuda_dev):
+    s = Setup(lib, cuda_dev, "e2m1", B=1, ctx=40, page=16, HKV=2, DQK=64, DV=64)
+    q, pos = s.cuda(s.normal(1, 1, 4, 64)), torch.tensor([[39]], dtype=torch.int32, device=cuda_dev)
+    for window, n_first in ((-2**32, 0), (-2**32 + 5, 0), (8, -2**32), (8, -2**32 + 4)):
+        with pytest.raises(lib.DSAError):
+            lib.dsa_cache_attn(q, s.cache, pos, window=window, n_first=n_first)
