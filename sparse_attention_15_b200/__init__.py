@@ -635,9 +635,9 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
         op = takes("out", out, (B, S, H, cache.dv))
     L, c = lib(), cache.ref
     window, n_first = _int(window), _int(n_first)
-    K = 0 if idx is None else idx.shape[-1]
+    K = None if idx is None else idx.shape[-1]
     ip = takes("idx", idx, (B, S, K), torch.int32)
-    sizes = (B, S, H, K, window, n_first)
+    sizes = (B, S, H, K, window, n_first)  # (K None: the window form, which no K stands for)
     nbytes = cache._workspaces.get(sizes)
     if nbytes is None:
         nbytes = int(L.dsa_cache_attn_workspace_bytes(c, B, S, H, window, n_first)

@@ -167,3 +167,25 @@ def test_a_window_past_an_int_is_refused_or_sees_every_key(lib):
                                        128, 128, 0, FAKE, None) == 1
     assert L.dsa_window_attn_first(1, FAKE, FAKE, FAKE, -TOP - 1, None, 0, 0.0, 8, 1, 64, 64, 4, 2,
                                    128, 128, 0, FAKE, None) == 1
+
+
+# ----------------------------------------------------------------------------- workspaces
+def test_the_two_forms_share_no_workspace_size(answers):
+    """A call over no selected keys, which the library refuses, leaves the size of the whole-context
+    workspace alone, and the other way round."""
+    q, pos = torch.zeros(2, 1, 4, 64, dtype=BF), torch.zeros(2, 1, dtype=torch.int32)
+    none = torch.zeros(2, 1, 0, dtype=torch.int32)
+    sizes = {"dsa_cache_attn_workspace_bytes": 4096, "dsa_cache_sparse_attn_workspace_bytes": 0}
+
+    class Sizes(Answers):
+        def __getattr__(self, name):
+            got = super().__getattr__(name)
+            return (lambda *args: (got(*args), sizes[name])[1]) if name in sizes else got
+
+    for first in (0, 1):
+        dsa._LIB, c = Sizes(), some_cache()
+        forms = [lambda: dsa.dsa_cache_sparse_attn(q, c, pos, none), lambda: dsa.dsa_cache_attn(q, c, pos)]
+        forms[first]()
+        forms[1 - first]()
+        assert dsa._LIB.last("dsa_cache_attn")[13] == 4096
+        assert dsa._LIB.last("dsa_cache_sparse_attn")[13] == 0

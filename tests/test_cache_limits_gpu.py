@@ -78,3 +78,15 @@ def test_cache_windows_below_an_int_are_refused(lib, cuda_dev):
     for window, n_first in ((-2**32, 0), (-2**32 + 5, 0), (8, -2**32), (8, -2**32 + 4)):
         with pytest.raises(lib.DSAError):
             lib.dsa_cache_attn(q, s.cache, pos, window=window, n_first=n_first)
+
+
+# ----------------------------------------------------------------------------- refused calls
+def test_a_refused_call_leaves_the_next_one_alone(lib, cuda_dev):
+    """No selected keys at all are refused; the whole context of the same rows is then as before."""
+    s = Setup(lib, cuda_dev, "e2m1", B=2, ctx=900, page=64, HKV=4, DQK=64, DV=64)
+    q = s.cuda(s.normal(2, 1, 8, 64))
+    pos = torch.tensor([[899], [500]], dtype=torch.int32, device=cuda_dev)
+    want = lib.dsa_cache_attn(q, lib.Cache(s.pages, s.table, 4, 64, 64), pos)
+    with pytest.raises(lib.DSAError):
+        lib.dsa_cache_sparse_attn(q, s.cache, pos, pos.new_empty(2, 1, 0))
+    assert torch.equal(lib.dsa_cache_attn(q, s.cache, pos), want)
