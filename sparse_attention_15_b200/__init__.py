@@ -515,7 +515,8 @@ def dsa_cache_pages(fmt, n_pages, page_size, kv_heads, dqk, dv, device="cuda"):
 class Cache:
     """A paged key/value cache (include/dsa.h, section 5): pages [n_pages, page_size, row] (bf16
     rows, or uint8 rows held in 4 bits) and the page table [B, max_pages] int32.  Holds the
-    tensors; the page table may be filled in place as sequences grow."""
+    tensors; the page table may be filled in place as sequences grow.  What it describes is fixed:
+    other tensors, or these resized, take a new Cache."""
 
     def __init__(self, pages, table, kv_heads, dqk, dv, k_scale=1.0, v_scale=1.0):
         _dev(pages, table)
@@ -540,11 +541,21 @@ class Cache:
         self.ref = ctypes.byref(self.args)
         self._bf16 = torch.empty(0, dtype=torch.bfloat16, device=self.device)  # outputs' kind
         self._workspaces = {}  # workspace bytes by the sizes of a call
+        self._at = (pages.data_ptr(), table.data_ptr(), table.shape)
+        self._fixed = True
+
+    def __setattr__(self, name, value):
+        # (the library reads its own copy, `args`: a new table here would not reach it)
+        if "_fixed" in self.__dict__:
+            raise AttributeError(f"a Cache is not changed ({name}): make a new one")
+        object.__setattr__(self, name, value)
 
     def _rows(self, pos):
         """(B, S) of a call with positions pos, which must suit the table and the current device."""
         if pos.dim() != 2 or pos.shape[0] != self.table.shape[0]:
             raise ValueError(f"pos is [B, S] with B = {self.table.shape[0]} (the table's rows)")
+        if (self.pages.data_ptr(), self.table.data_ptr(), self.table.shape) != self._at:
+            raise ValueError("the cache's tensors were moved or resized: make a new Cache")
         if self.device.index != torch.cuda.current_device():
             raise ValueError(f"the cache is on {self.device}, which is not the current device")
         self._takes("pos", pos, pos.shape, torch.int32)

@@ -189,3 +189,31 @@ def test_the_two_forms_share_no_workspace_size(answers):
         forms[1 - first]()
         assert dsa._LIB.last("dsa_cache_attn")[13] == 4096
         assert dsa._LIB.last("dsa_cache_sparse_attn")[13] == 0
+
+
+# ----------------------------------------------------------------------------- a cache's tensors
+def test_a_cache_is_not_changed(answers):
+    """Another page table, or other sizes, would not reach the library: they take a new Cache."""
+    c, pos = some_cache(), torch.zeros(2, 1, dtype=torch.int32)
+    for name, value in (("table", torch.zeros(2, 9, dtype=torch.int32)), ("pages", c.pages.clone()),
+                        ("kv_heads", 1), ("dqk", 128), ("device", "cpu"), ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(c, name, value)
+    dsa.dsa_cache_read(c, pos)
+    c.table[:] = 3  # the entries may change
+    dsa.dsa_cache_read(c, pos)
+
+
+@pytest.mark.parametrize("which,shape", [("table", (2, 3)), ("table", (2, 4000)),
+                                         ("pages", (800, 16, 144))])
+def test_a_cache_whose_tensors_were_resized_is_refused(answers, which, shape):
+    c, pos = some_cache(), torch.zeros(2, 1, dtype=torch.int32)
+    q, new = torch.zeros(2, 1, 4, 64, dtype=BF), torch.zeros(2, 1, 2, 64, dtype=BF)
+    getattr(c, which).resize_(shape)
+    n = len(answers.calls)
+    for call in (lambda: dsa.dsa_cache_append(c, pos, new, new), lambda: dsa.dsa_cache_read(c, pos),
+                 lambda: dsa.dsa_cache_attn(q, c, pos),
+                 lambda: dsa.dsa_cache_sparse_attn(q, c, pos, pos[..., None])):
+        with pytest.raises(ValueError):
+            call()
+    assert len(answers.calls) == n
