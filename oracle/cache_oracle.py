@@ -45,9 +45,12 @@ def _nearest_even(v, table):
 
 
 def encode(x, tensor_scale):
-    """x [..., D] -> (codes [..., D] 0..15, scales [..., D/16] e4m3 bytes)."""
-    y = (np.asarray(x).astype(np.float32) / np.float32(tensor_scale)).reshape(*x.shape[:-1], -1, 16)
-    bad = ~np.isfinite(y).all(-1)
+    """x [..., D] -> (codes [..., D] 0..15, scales [..., D/16] e4m3 bytes).  A group with a NaN or an
+    infinity has a NaN scale; a quotient past float32's range saturates."""
+    with np.errstate(over="ignore"):
+        y = np.asarray(x).astype(np.float32) / np.float32(tensor_scale)
+    y = y.reshape(*x.shape[:-1], -1, 16)
+    bad = ~np.isfinite(np.asarray(x)).reshape(y.shape).all(-1)
     y = np.where(bad[..., None], np.float32(0), y)
     s8 = _nearest_even((np.abs(y).max(-1) / np.float32(6)).astype(np.float64), E4M3)
     s = E4M3[s8].astype(np.float32)[..., None]

@@ -16,13 +16,13 @@
 // (rounded to nearest even, saturated at 6).  Keys are taken as bf16 holds them, so a 4-bit cache
 // holds the quantised rows of the bf16 cache.  Every operation is one correctly rounded float32
 // operation, so codes and scales are reproducible to the bit.  4 bits hold no infinity or NaN: a
-// group with one gets a NaN scale and reads back as NaN.
+// group with one among its x gets a NaN scale and reads back as NaN.  (A finite x whose y is past
+// float32's range saturates like any other.)
 //
 // Memory-bound in bf16 (8192 tokens of 32 heads, 520 MB: 90 us, 5.8 TB/s); in 4 bits (2 x 4001 tokens
 // of 8 heads, 246 MB: 60 us, 4.1 TB/s) latency and the encoding's instructions show.  A thread takes
 // a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's maximum needs no exchange; a
 // half-split thread takes both groups of its pairs.
-#include <float.h>
 #include <math.h>
 
 #include "cache.cuh"
@@ -189,6 +189,15 @@ struct Encoded {
   uint2 codes;
   uint32_t scale;
 };
+// Whether no value of the group is an infinity or NaN (an exponent field of ones).
+__device__ __forceinline__ bool all_finite(const Group& x) {
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    finite = finite && (word(x, i) & 0x7f800000u) != 0x7f800000u &&
+             (word(x, i) & 0x7f80u) != 0x7f80u;
+  return finite;
+}
 // `inv` the reciprocal of a scale that is a power of two.
 __device__ __forceinline__ Encoded encode_group(const Group& x, float inv) {
   float y[16], top = 0.f;
@@ -197,12 +206,9 @@ __device__ __forceinline__ Encoded encode_group(const Group& x, float inv) {
     y[2 * i] = lo_f(word(x, i)) * inv;
     y[2 * i + 1] = hi_f(word(x, i)) * inv;
   }
-  bool finite = true;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    top = fmaxf(top, fabsf(y[i]));
-    finite = finite && fabsf(y[i]) <= FLT_MAX;
-  }
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+  const bool finite = all_finite(x);
   float s;
   Encoded e;
   e.scale = e4m3_of(__fdiv_rn(top, 6.0f), &s);
@@ -220,13 +226,12 @@ __device__ __forceinline__ Encoded encode_group(const Group& x, float inv) {
 // Any scale: true divisions, out of the way (32 of them).
 __device__ __noinline__ Encoded encode_group_by_division(const Group& x, float tensor_scale) {
   float top = 0.f;
-  bool finite = true;
   for (int i = 0; i < 8; ++i) {
     const float a = __fdiv_rn(lo_f(word(x, i)), tensor_scale);
     const float b = __fdiv_rn(hi_f(word(x, i)), tensor_scale);
     top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
-    finite = finite && fabsf(a) <= FLT_MAX && fabsf(b) <= FLT_MAX;
   }
+  const bool finite = all_finite(x);
   float s;
   Encoded e;
   e.scale = e4m3_of(__fdiv_rn(top, 6.0f), &s);

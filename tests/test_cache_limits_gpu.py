@@ -1,9 +1,11 @@
 """The paged cache on the GPU at the borders of its arguments: calls side by side on several streams,
 the largest groups of heads, and values and scales at the ends of their types.  Setup, oracle and
 tolerances are those of test_cache_gpu."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import cache_oracle as O
 from test_cache_gpu import BF, Setup
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +92,32 @@ def test_a_refused_call_leaves_the_next_one_alone(lib, cuda_dev):
     with pytest.raises(lib.DSAError):
         lib.dsa_cache_sparse_attn(q, s.cache, pos, pos.new_empty(2, 1, 0))
     assert torch.equal(lib.dsa_cache_attn(q, s.cache, pos), want)
+
+
+# ----------------------------------------------------------------------------- values and scales
+@pytest.mark.parametrize("k_scale,v_scale", [(0.25, 0.3), (0.3, 2.0**-20), (2.0**-90, 1e-30)])
+def test_values_past_the_range_of_a_quotient_saturate(lib, cuda_dev, k_scale, v_scale):
+    """Finite values whose quotient by the tensor's scale float32 does not hold: codes of 6 and scales
+    of 448, as where the quotient is merely large; NaN is for infinities and NaN alone."""
+    s = Setup(lib, cuda_dev, "e2m1", B=1, ctx=4, page=4, HKV=2, DQK=64, DV=64, k_scale=k_scale,
+              v_scale=v_scale, fill=False)
+    k, v = s.normal(1, 4, 2, 64), s.normal(1, 4, 2, 64)
+    for x in (k, v):
+        x[0, 0, 0, 3], x[0, 0, 0, 20] = 3.3e38, -3.3e38
+        x[0, 0, 1, :16] = np.linspace(-3.3e38, 3.3e38, 16)
+        x[0, 1, 0] = np.ldexp(1.5, np.arange(64) * 4 - 126)
+        x[0, 1, 1, 5], x[0, 1, 1, 6] = np.inf, 3e38
+        x[0, 2, 0, 40], x[0, 2, 0, 41], x[0, 2, 1, 0] = np.nan, 1e38, -np.inf
+    k, v = O.to_bf16(k), O.to_bf16(v)
+    pos = torch.arange(4, dtype=torch.int32, device=cuda_dev)[None]
+    lib.dsa_cache_append(s.cache, pos, s.cuda(k), s.cuda(v))
+    rows = s.pages[s.table[0, 0].item()].cpu().numpy()
+    for t in range(4):
+        want, kd, vd = O.row_of(k[0, t], v[0, t], "e2m1", k_scale, v_scale)
+        assert np.array_equal(rows[t][:144], want[:144])
+        assert np.isfinite(kd).all() == np.isfinite(k[0, t]).all()
+    # read back: 6 * 448 * scale of a saturated group's largest, in bf16
+    k2, _ = lib.dsa_cache_read(s.cache, pos)
+    top = float(torch.tensor(6 * 448 * float(np.float32(k_scale)), dtype=torch.float32).to(BF))
+    assert k2[0, 0, 0, 3].item() == top and k2[0, 0, 0, 20].item() == -top
+    assert k2[0, 1, 1, :16].isnan().all() and not k2[0, 1, 1, 16:].isnan().any()
