@@ -707,10 +707,14 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
       }
       const int h = hg * heads + hl;
       if (alone) {
-        float f = L > 0.f ? a.c.v_scale / L : 0.f;
-        if (a.gate) f *= gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode);
-        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * f, x[1] * f);
-        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * f, x[3] * f);
+        // (the mean before the tensor's scale and the gate: their product with 1 / L may underflow)
+        const float f = L > 0.f ? 1.0f / L : 0.f;
+        const float gt =
+            a.gate ? gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode) : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = x[e] * f * a.c.v_scale * gt;
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2], x[3]);
         uint2 y;
         y.x = *reinterpret_cast<const uint32_t*>(&y0);
         y.y = *reinterpret_cast<const uint32_t*>(&y1);
@@ -791,9 +795,9 @@ __global__ void __launch_bounds__(DV) cache_merge_kernel(const CacheAttnArgs a) 
       x = fmaf(po[(q + p) * step * DV], weight[p].x, x);
     }
   }
-  float f = L > 0.f ? a.c.v_scale / L : 0.f;
-  if (a.gate) f *= gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode);
-  *out = __float2bfloat16_rn(x * f);
+  x = x * (L > 0.f ? 1.0f / L : 0.f) * a.c.v_scale;
+  if (a.gate) x *= gate_act(__bfloat162float(a.gate[(size_t)row * a.H + h]), a.gate_mode);
+  *out = __float2bfloat16_rn(x);
 }
 
 // How a call is laid out over CTAs.

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import cache_oracle as O
-from test_cache_gpu import BF, Setup
+from test_cache_gpu import BF, Setup, check
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,30 @@ def test_values_past_the_range_of_a_quotient_saturate(lib, cuda_dev, k_scale, v_
     top = float(torch.tensor(6 * 448 * float(np.float32(k_scale)), dtype=torch.float32).to(BF))
     assert k2[0, 0, 0, 3].item() == top and k2[0, 0, 0, 20].item() == -top
     assert k2[0, 1, 1, :16].isnan().all() and not k2[0, 1, 1, 16:].isnan().any()
+
+
+@pytest.mark.parametrize("v_scale", [2.0**-120, 2.0**-126, 2.0**100])
+@pytest.mark.parametrize("S,ctx,low", [(1, 2500, 1), (1200, 40, 1), (1200, 2000, 64)])
+def test_a_small_tensor_scale_keeps_the_output(lib, cuda_dev, v_scale, S, ctx, low):
+    """Large sums of probabilities (the most where the first steps' scores are 8 lower in log2 units
+    than the others) beside a scale at the end of float32's range: neither 1 / L times the scale nor the
+    scale times the gate is what the output is.  Rows in pieces, and rows taken whole."""
+    s = Setup(lib, cuda_dev, "e2m1", B=1, ctx=ctx, page=64, HKV=1, DQK=64, DV=64, v_scale=v_scale,
+              fill=False)
+    k = np.zeros((1, ctx, 1, 64))
+    k[0, low:] = 6.0  # exact in 4 bits; the first keys' scores are 0, the others' 8 in log2 units
+    v = O.to_bf16(s.normal(1, ctx, 1, 64) * v_scale)  # (what the call gets, below 2^-126 too)
+    every = torch.arange(ctx, dtype=torch.int32, device=cuda_dev)[None]
+    lib.dsa_cache_append(s.cache, every, s.cuda(k), s.cuda(v))
+    for t in range(ctx):
+        _, s.k[0, t], s.v[0, t] = O.row_of(k[0, t], v[0, t], "e2m1", 1.0, v_scale)
+    q = np.full((4, 64), 1.0)
+    gate = np.array([-20.0, 0.0, 1.0, 5.0])
+    sm = 8 * np.log(2) / (6.0 * 64)
+    pos = torch.full((1, S), ctx - 1, dtype=torch.int32, device=cuda_dev)
+    rows = lambda x: s.cuda(np.broadcast_to(x, (1, S, *x.shape)).copy())  # noqa: E731
+    out = lib.dsa_cache_attn(rows(q), s.cache, pos, gate=rows(gate), sm_scale=sm)
+    want, mag = O.attend(q, s.k[0], s.v[0], list(range(ctx)), float(np.float32(sm)), gate)
+    # below bf16's and float32's normal range a result is off by half a step of it
+    for i in {0, S // 2, S - 1}:
+        check(out[0, i], want, mag, floor=2.0**-134 + 3 * 2.0**-150)
