@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import cache_oracle as O
-from test_cache_gpu import BF, Setup, check
+from test_cache_gpu import BF, Setup, check, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,27 @@ def test_a_small_tensor_scale_keeps_the_output(lib, cuda_dev, v_scale, S, ctx, l
     # below bf16's and float32's normal range a result is off by half a step of it
     for i in {0, S // 2, S - 1}:
         check(out[0, i], want, mag, floor=2.0**-134 + 3 * 2.0**-150)
+
+
+# ----------------------------------------------------------------------------- groups of heads
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("G,DQK,DV", [(33, 192, 128), (40, 192, 128), (41, 64, 64), (48, 128, 64),
+                                      (56, 64, 128), (57, 192, 64), (64, 192, 128), (64, 128, 128)])
+def test_more_than_32_heads_of_one_key_head(lib, cuda_dev, fmt, G, DQK, DV):
+    """Groups of five to eight times 8 heads, with more warps than the formats' usual CTA: whole
+    contexts in many pieces and in one, a window, selected keys, rows in plenty."""
+    s = Setup(lib, cuda_dev, fmt, B=2, ctx=700, page=48, HKV=1, DQK=DQK, DV=DV,
+              k_scale=1.0 if fmt == "bf16" else 0.5, v_scale=1.0 if fmt == "bf16" else 2.0)
+    run_attn(s, np.array([[699], [17]]), G, gate=True)
+    run_attn(s, np.array([[699], [-1]]), G, window=100, n_first=9)
+    idx = np.full((2, 1, 333), -1)
+    for b in range(2):
+        idx[b, 0, :200] = np.sort(s.r.permutation(700)[:200])
+    run_attn(s, np.array([[650], [300]]), G, idx=idx)
+    run_attn(s, s.r.integers(-1, 700, (2, 620)), G, window=3)
+
+
+def test_two_key_heads_of_32_heads(lib, cuda_dev):
+    for fmt in ("bf16", "e2m1"):
+        s = Setup(lib, cuda_dev, fmt, B=1, ctx=900, page=100, HKV=2, DQK=192, DV=128)
+        run_attn(s, np.array([[899]]), 64, gate=True, gate_mode="silu")
