@@ -181,7 +181,8 @@ def _own(shape, dtype, device, stream, returned=True):
 def _int(x):
     """An argument as a C int: past its range the end of the range (ctypes would wrap it), which the
     library refuses, or takes as a window or a number of keys that covers every key."""
-    return max(-_INT_MAX - 1, min(int(x), _INT_MAX))
+    x = int(x)
+    return x if -_INT_MAX <= x <= _INT_MAX else _INT_MAX if x > 0 else -_INT_MAX - 1
 
 
 def _dev(*ts):
@@ -541,7 +542,9 @@ class Cache:
         self.ref = ctypes.byref(self.args)
         self._bf16 = torch.empty(0, dtype=torch.bfloat16, device=self.device)  # outputs' kind
         self._workspaces = {}  # workspace bytes by the sizes of a call
-        self._at = (pages.data_ptr(), table.data_ptr(), table.shape)
+        self._pages_at, self._table_at = pages.data_ptr(), table.data_ptr()
+        self._B, self._entries = table.shape[0], table.numel()
+        self._device_index = self.device.index
         self._fixed = True
 
     def __setattr__(self, name, value):
@@ -552,14 +555,16 @@ class Cache:
 
     def _rows(self, pos):
         """(B, S) of a call with positions pos, which must suit the table and the current device."""
-        if pos.dim() != 2 or pos.shape[0] != self.table.shape[0]:
-            raise ValueError(f"pos is [B, S] with B = {self.table.shape[0]} (the table's rows)")
-        if (self.pages.data_ptr(), self.table.data_ptr(), self.table.shape) != self._at:
+        shape, table = pos.shape, self.table
+        if len(shape) != 2 or shape[0] != self._B:
+            raise ValueError(f"pos is [B, S] with B = {self._B} (the table's rows)")
+        if self.pages.data_ptr() != self._pages_at or table.data_ptr() != self._table_at or \
+                table.numel() != self._entries:
             raise ValueError("the cache's tensors were moved or resized: make a new Cache")
-        if self.device.index != torch.cuda.current_device():
+        if self._device_index != torch.cuda.current_device():
             raise ValueError(f"the cache is on {self.device}, which is not the current device")
-        self._takes("pos", pos, pos.shape, torch.int32)
-        return pos.shape
+        self._takes("pos", pos, shape, torch.int32)
+        return shape
 
     def _output(self, shape, stream):
         """A call's bf16 output (new_empty is the cheaper call, by 1 us)."""
