@@ -614,7 +614,7 @@ def dsa_cache_append(cache, pos, k, v, rope="off", inv_freq=None, q=None, q_out=
             qs = (B, S, H, cache.dqk)
             qp = takes("q", q, qs)
             if q_out is None:
-                q_out = _own(qs, q.dtype, q.device, stream)
+                q_out = cache._output(qs, stream)
             qo = takes("q_out", q_out, qs)
         elif q_out is not None:
             raise ValueError("q_out goes with q")
