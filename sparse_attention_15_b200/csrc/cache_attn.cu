@@ -30,15 +30,18 @@
 // e4m3 scale has 6 significant bits and stays in f16's normal range.  Queries become f16 after a
 // scaling of each head by a power of two (its largest element to [2^13, 2^14)): exact for every
 // element within 2^-30 of the largest (8 bits into 11), and off by 2^-38 of it at most otherwise.
-// Probabilities are f16 with the running maximum at 2^6 (so terms down to 2^-30 of the largest
-// stay): half a step is 2^-11 each, below the rounding of the output.
+// Probabilities are f16 pairs hi + lo with the running maximum at 2^6 (so terms down to 2^-30 of the
+// largest stay): 22 bits, as one f16's 11 would show wherever the values cancel.  Warps of up to 4
+// query heads have them twice, in the columns 0..3 and 4..7, and the second four take lo: the pair
+// costs no product (64 x 2048 keys: 206 us, one f16 201 us, two products 219 us).  Warps of 5 to 8
+// heads take two products, as bf16 rows do.
 //
 // Measured: 64 x 2048 selected keys of 32 heads (755 MB) in 180 us, 4.2 TB/s; eight contexts of up to
 // 131072 tokens and 8 heads (1.13 GB) in 250-260 us, 4.4 TB/s.
 //
 // bf16 rows are bound by the bandwidth (16 x 2048 keys of 32 heads, 671 MB: 121 us, 5.5 TB/s).  They
-// are used as they are; probabilities are a bf16 pair hi + lo, as one bf16 would be no more exact than
-// the output.
+// are used as they are; probabilities are a bf16 pair, as one bf16 would be no more exact than the
+// output.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -293,7 +296,17 @@ __device__ __forceinline__ void softmax_step(const float (&x)[4], float (&m)[2],
   l[1] += p[1] + p[3];
 }
 
-template <int FMT, int DQK, int DV>
+// Two float32 values in f16; with `rest`, what their f16 values `h` leave of them.
+__device__ __forceinline__ __half2 without(const float* p, __half2 h, bool rest) {
+  uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+  w &= rest ? 0xffffffffu : 0u;
+  h = *reinterpret_cast<const __half2*>(&w);
+  return __floats2half2_rn(p[0] - __low2float(h), p[1] - __high2float(h));
+}
+
+// FEW (4 bits): at most 4 query heads to a warp, which the columns 4..7 hold a second time for the
+// lo halves of the probabilities.
+template <int FMT, int DQK, int DV, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::WARPS == 8 ? 2 : 1))
     cache_attn_kernel(const CacheAttnArgs a) {
   using S = Slot<FMT, DQK, DV>;
@@ -454,9 +467,10 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
     uint32_t qf[QC][8];
     float cs[2] = {a.qk_scale, a.qk_scale};  // score scale of columns 2t, 2t + 1
     {
-      const bool has = g < ncol;
+      const int head = FEW ? g & 3 : g;
+      const bool has = head < ncol;
       const uint4* qp = reinterpret_cast<const uint4*>(
-          a.q + ((size_t)row * a.H + (has ? h0 + g : 0)) * DQK + 16 * t4);
+          a.q + ((size_t)row * a.H + (has ? h0 + head : 0)) * DQK + 16 * t4);
 #pragma unroll
       for (int c = 0; c < QC; ++c)
 #pragma unroll
@@ -555,7 +569,17 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
         }
         float p[4];
         softmax_step<TOP, MT>(x, m, l, o, p);
-        const __half2 p01 = __floats2half2_rn(p[0], p[1]), p23 = __floats2half2_rn(p[2], p[3]);
+        // probabilities hi + lo: in the columns 0..3 and 4..7, or in two products
+        __half2 p01 = __floats2half2_rn(p[0], p[1]), p23 = __floats2half2_rn(p[2], p[3]);
+        uint32_t c0, c1;
+        if constexpr (FEW) {
+          p01 = without(p, p01, t4 >= 2);
+          p23 = without(p + 2, p23, t4 >= 2);
+        } else {
+          const __half2 r01 = without(p, p01, true), r23 = without(p + 2, p23, true);
+          c0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&r01));
+          c1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&r23));
+        }
         const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p01));
         const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p23));
         const uint32_t s01 = e4m3x2_to_f16(sc0), s23 = e4m3x2_to_f16(sc1);
@@ -573,6 +597,7 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
             const uint32_t f[4] = {mul_f16x2(e01[i], s01), mul_f16x2(o01[i], s01),
                                    mul_f16x2(e23[i], s23), mul_f16x2(o23[i], s23)};
             mma_f16(o[4 * w + i], f, b0, b1);
+            if constexpr (!FEW) mma_f16(o[4 * w + i], f, c0, c1);
           }
         }
       } else {
@@ -701,7 +726,11 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
         const float mk = ml[w * 16 + col * 2];
         const float f = mk == -INFINITY ? 0.f : ex2_ftz(mk - M);
         L = fmaf(ml[w * 16 + col * 2 + 1], f, L);
-        const float4 v = *reinterpret_cast<const float4*>(ob + (size_t)(w * 8 + col) * DV + d);
+        float4 v = *reinterpret_cast<const float4*>(ob + (size_t)(w * 8 + col) * DV + d);
+        if constexpr (FEW) {  // the columns 4..7 hold the lo products of 0..3
+          const float4 y = *reinterpret_cast<const float4*>(ob + (size_t)(w * 8 + col + 4) * DV + d);
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
         x[0] = fmaf(v.x, f, x[0]); x[1] = fmaf(v.y, f, x[1]);
         x[2] = fmaf(v.z, f, x[2]); x[3] = fmaf(v.w, f, x[3]);
       }
@@ -892,13 +921,15 @@ bool plan_of(const CacheAttnProblem& p, Plan* pl) {
 template <int FMT, int DQK, int DV>
 cudaError_t launch(const CacheAttnArgs& a, const Plan& p, Ring<FMT, DQK, DV>, cudaStream_t st) {
   const int smem = Ring<FMT, DQK, DV>::smem(p.nw);
-  auto kern = cache_attn_kernel<FMT, DQK, DV>;
+  const bool few = FMT == 1 && a.G <= 4;
+  auto kern = few ? cache_attn_kernel<FMT, DQK, DV, FMT == 1> : cache_attn_kernel<FMT, DQK, DV, false>;
   const dim3 grid = p.shares > 0 ? dim3((unsigned)p.nhg, (unsigned)p.shares)
                     : p.grid > 0 ? dim3((unsigned)p.grid)
                                  : dim3((unsigned)a.rows * (unsigned)p.nhg);
   // The kernel's attributes are set once per device (each call of theirs costs a host microsecond),
   // and again if a launch finds them gone, as after a device reset.
-  static std::atomic<unsigned long long> ready{0};
+  static std::atomic<unsigned long long> ready_of[2];
+  std::atomic<unsigned long long>& ready = ready_of[few];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

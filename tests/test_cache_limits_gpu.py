@@ -172,3 +172,28 @@ def test_two_key_heads_of_32_heads(lib, cuda_dev):
     for fmt in ("bf16", "e2m1"):
         s = Setup(lib, cuda_dev, fmt, B=1, ctx=900, page=100, HKV=2, DQK=192, DV=128)
         run_attn(s, np.array([[899]]), 64, gate=True, gate_mode="silu")
+
+
+# ----------------------------------------------------------------------------- probabilities
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("HKV,G", [(8, 1), (2, 3), (8, 4), (2, 5), (4, 8), (2, 12)])
+def test_values_that_cancel(lib, cuda_dev, fmt, HKV, G):
+    """Two keys of nearly equal scores whose values are c and -c: the output is c times the difference
+    of the probabilities, tanh of half the scores' difference (keys and c as the cache holds them).  One dim of q alone is not zero, so scores are
+    one product, below 2^3 in log2 units: float32 roundings (2^3 * 2^-24 * 3) and an exponential within
+    2^-22 give p within 2^-19, and a pair of bf16 holds it within 2^-17 (of f16 within 2^-21)."""
+    s = Setup(lib, cuda_dev, fmt, B=1, ctx=2, page=16, HKV=HKV, DQK=64, DV=64, fill=False)
+    k, v = np.zeros((1, 2, HKV, 64)), np.ones((1, 2, HKV, 64))
+    k[0, 0, :, 0], k[0, 1, :, 0], v[0, 1] = 6.0, 4.0, -1.0
+    every = torch.tensor([[0, 1]], dtype=torch.int32, device=cuda_dev)
+    lib.dsa_cache_append(s.cache, every, s.cuda(k), s.cuda(v))
+    H, n = HKV * G, 40
+    q = np.zeros((n, H, 64))
+    q[..., 0] = O.to_bf16(2.0 ** s.r.uniform(-7, -3, (n, H)))
+    pos = torch.ones(1, n, dtype=torch.int32, device=cuda_dev)
+    out = lib.dsa_cache_attn(s.cuda(q[None]), s.cache, pos, sm_scale=1.0)[0].double().cpu().numpy()
+    (_, k0, v0), (_, k1, v1) = (O.row_of(k[0, t], v[0, t], fmt, 1.0, 1.0) for t in range(2))
+    c = v0[0, 0]
+    assert (v0 == c).all() and (v1 == -c).all() and c < 1.04
+    want = c * np.tanh(q[..., :1] * (k0 - k1)[0, 0] / 2)
+    assert (np.abs(out - want) <= want * 2.0**-8 + 2.0**-16).all()
