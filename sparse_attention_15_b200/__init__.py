@@ -185,10 +185,19 @@ def _int(x):
     return x if -_INT_MAX <= x <= _INT_MAX else _INT_MAX if x > 0 else -_INT_MAX - 1
 
 
-def _dev(*ts):
+def _cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("libdsa takes contiguous CUDA tensors")
+
+
+def _dev(*ts):
+    """A call's tensors: contiguous, and on the current device, where its kernels run."""
+    _cuda(*ts)
+    current = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"a tensor is on {t.device}, which is not the current device")
 
 
 def _dtype_code(t):
@@ -520,7 +529,7 @@ class Cache:
     other tensors, or these resized, take a new Cache."""
 
     def __init__(self, pages, table, kv_heads, dqk, dv, k_scale=1.0, v_scale=1.0):
-        _dev(pages, table)
+        _cuda(pages, table)
         fmt = {torch.bfloat16: "bf16", torch.uint8: "e2m1"}.get(pages.dtype)
         if fmt is None:
             raise ValueError("pages are bf16, or uint8 for the 4-bit format")

@@ -62,6 +62,7 @@ def answers(monkeypatch):
 
     monkeypatch.setattr(dsa, "_LIB", a)
     monkeypatch.setattr(dsa, "_dev", lambda *ts: None)
+    monkeypatch.setattr(dsa, "_cuda", lambda *ts: None)
     monkeypatch.setattr(torch, "empty", made)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream)
@@ -217,3 +218,31 @@ def test_a_cache_whose_tensors_were_resized_is_refused(answers, which, shape):
         with pytest.raises(ValueError):
             call()
     assert len(answers.calls) == n
+
+
+# ----------------------------------------------------------------------------- devices
+class On:
+    """As much of a CUDA tensor as the binding's check looks at."""
+    is_cuda = True
+
+    def __init__(self, index):
+        self.index, self.device = index, f"cuda:{index}"
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels run on the current device, which may not reach another one's memory."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    dsa._dev(On(1), None, On(1))
+    for ts in ((On(0),), (On(1), On(0)), (None, On(1), On(2))):
+        with pytest.raises(ValueError, match="not the current device"):
+            dsa._dev(*ts)
+    for call in (lambda: dsa.dsa_window_attn(On(1), On(0), On(0), 8, n_first=4),
+                 lambda: dsa.dsa_topk(On(0), 4)):
+        with pytest.raises(ValueError, match="not the current device"):
+            call()
