@@ -9,6 +9,7 @@ fallback -- if libdsa.so is missing, importing a function raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -198,6 +199,13 @@ def _dev(*ts):
     for t in ts:
         if t is not None and t.get_device() != current:
             raise ValueError(f"a tensor is on {t.device}, which is not the current device")
+
+
+def _fits(name, t, shape, dtype):
+    """An argument that the library reads or writes as a contiguous `shape` of `dtype`: at least as
+    many elements (a larger buffer of the caller's is fine)."""
+    if t is not None and (t.dtype != dtype or t.numel() < math.prod(shape)):
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}: expected {tuple(shape)} {dtype}")
 
 
 def _dtype_code(t):
@@ -486,6 +494,16 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
     B, S, H, DQK = q.shape
     T, HKV, DV = k.shape[1], k.shape[2], v.shape[-1]
     gm = GATE[gate_mode or ("sigmoid" if gate is not None else "off")]
+    if k.shape[1:] != (T, HKV, DQK) or v.shape[1:] != (T, HKV, DV):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go with q {tuple(q.shape)}"
+                         " or with each other")
+    if (sink_k is None) != (sink_v is None):
+        raise ValueError("sink_k and sink_v go together")
+    NS = 0 if sink_k is None else sink_k.shape[0]
+    for name, t, shape in (("k", k, (B, T, HKV, DQK)), ("v", v, (B, T, HKV, DV)),
+                           ("gate", gate, (B, S, H)), ("out", out, (B, S, H, DV)),
+                           ("sink_k", sink_k, (NS, HKV, DQK)), ("sink_v", sink_v, (NS, HKV, DV))):
+        _fits(name, t, shape, q.dtype)
     if out is None:
         out = _own((B, S, H, DV), q.dtype, q.device, stream)
     if n_first:
@@ -499,7 +517,7 @@ def dsa_window_attn(q, k, v, window, gate=None, gate_mode=None, sm_scale=0.0, al
                                      ATTN_ALGO[algo], _ptr(out), _stream(stream)))
     else:
         _check(lib().dsa_window_attn_sinks(_dtype_code(q), _ptr(q), _ptr(k), _ptr(v),
-                                           _ptr(sink_k), _ptr(sink_v), int(sink_k.shape[0]),
+                                           _ptr(sink_k), _ptr(sink_v), NS,
                                            _ptr(gate), gm, float(sm_scale), window, B, S,
                                            T, H, HKV, DQK, DV, ATTN_ALGO[algo], _ptr(out),
                                            _stream(stream)))

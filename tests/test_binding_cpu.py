@@ -246,3 +246,28 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                  lambda: dsa.dsa_topk(On(0), 4)):
         with pytest.raises(ValueError, match="not the current device"):
             call()
+
+
+# ----------------------------------------------------------------------------- shapes and types
+def test_window_attn_refuses_tensors_that_do_not_go_together(answers):
+    """What the library would read or write past the end, or as another type."""
+    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    q, k, v = z(2, 3, 4, 64), z(2, 32, 2, 64), z(2, 32, 2, 128)
+    good = dict(gate=z(2, 3, 4), out=z(2, 3, 4, 128))
+    for more in (dict(n_first=4), dict(), dict(sink_k=z(5, 2, 64), sink_v=z(5, 2, 128))):
+        dsa.dsa_window_attn(q, k, v, 8, **good, **more)
+    dsa.dsa_window_attn(q, z(3, 32, 2, 64), z(3, 32, 2, 128), 8, out=z(9, 3, 4, 128))  # room to spare
+    n = len(answers.calls)
+    f32 = torch.float32
+    bad = [dict(k=z(1, 32, 2, 64)), dict(k=z(2, 31, 2, 64)), dict(k=z(2, 32, 2, 128)),
+           dict(k=z(2, 32, 2, 64, dtype=f32)), dict(q=z(2, 3, 4, 64, dtype=f32)),
+           dict(v=z(2, 32, 1, 128)), dict(v=z(1, 32, 2, 128)), dict(v=z(2, 32, 2, 128, dtype=f32)),
+           dict(gate=z(2, 3, 3)), dict(gate=z(2, 3, 4, dtype=f32)), dict(out=z(2, 3, 4, 64)),
+           dict(out=z(2, 3, 4, 128, dtype=f32)), dict(sink_k=z(5, 2, 64)),
+           dict(sink_k=z(5, 2, 64), sink_v=z(4, 2, 128)), dict(sink_k=z(5, 1, 64), sink_v=z(5, 2, 128))]
+    for change in bad:
+        for n_first in (0, 4):
+            args = dict(dict(q=q, k=k, v=v), **change)
+            with pytest.raises(ValueError):
+                dsa.dsa_window_attn(window=8, n_first=n_first, **args)
+    assert len(answers.calls) == n
