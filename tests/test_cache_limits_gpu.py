@@ -197,3 +197,40 @@ def test_values_that_cancel(lib, cuda_dev, fmt, HKV, G):
     assert (v0 == c).all() and (v1 == -c).all() and c < 1.04
     want = c * np.tanh(q[..., :1] * (k0 - k1)[0, 0] / 2)
     assert (np.abs(out - want) <= want * 2.0**-8 + 2.0**-16).all()
+
+
+# ----------------------------------------------------------------------------- graphs
+def test_graphs_with_side_streams_and_at_the_same_time(lib, cuda_dev):
+    """A step whose layers run on two streams, captured twice with the workspaces that the binding
+    allocates, and both graphs replayed at the same time: each gives its own queries' results."""
+    s = Setup(lib, cuda_dev, "e2m1", B=2, ctx=900, page=64, HKV=4, DQK=64, DV=64)
+    pos = torch.tensor([[899], [500]], dtype=torch.int32, device=cuda_dev)
+    idx = torch.arange(0, 900, 3, dtype=torch.int32, device=cuda_dev).expand(2, 1, -1).contiguous()
+    side = torch.cuda.Stream()
+
+    def step(q):
+        side.wait_stream(torch.cuda.current_stream())
+        a = lib.dsa_cache_attn(q, s.cache, pos)
+        b = lib.dsa_cache_sparse_attn(q, s.cache, pos, idx, stream=side)
+        c, _ = lib.dsa_cache_read(s.cache, pos, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        return a, b, c
+
+    qs = [s.cuda(s.normal(2, 1, 8, 64)) for _ in range(2)]
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(step(q))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for got, right in zip(held, want):
+        for x, y in zip(got, right):
+            assert torch.equal(x, y)
