@@ -438,7 +438,8 @@ size_t dsa_cache_row_bytes(dsa_cache_format format, int HKV, int DQK, int DV);
  *   k_out  [B,S,HKV,DQK] out: the rotated keys as well, or NULL; may be k
  *   4-bit rows: y = x / k_scale (v_scale); a group's scale is e4m3(max|y| / 6), to nearest and at
  *   most 448; a code is e2m1(y / scale), to nearest even and at most 6; each operation one float32
- *   operation, x the (rotated) bf16 value.  A group with a NaN or an infinity reads back as NaN.
+ *   operation, x the (rotated) bf16 value.  A group with a NaN or an infinity among its x reads back
+ *   as NaN.
  *   A padding token (pos < 0) is not stored and gets zeros in q_out and k_out; a token without a
  *   page is rotated but not stored.  Rows of other tokens are left as they were.  Two tokens of one
  *   call must not have the same place in the cache: what that row then holds is unspecified.
@@ -457,7 +458,11 @@ dsa_status dsa_cache_read(const dsa_cache* cache, const int32_t* pos, int B, int
 /* 5c. Attention of the tokens q [B,S,H,DQK] at pos over the cache: of each sequence's whole context
  *    (window == 0: keys t <= pos), or of a sliding window with visible first tokens (t <= pos and
  *    t > pos - window or t < n_first).  Query head h reads KV head h / (H/HKV).  For decode: one or
- *    a few tokens per sequence, each reading its own keys.
+ *    a few tokens per sequence, each reading its own keys.  From 64 tokens of a sequence on (a
+ *    prompt's next part behind a cached prefix) reading the visible tokens back and running
+ *    dsa_window_attn over them is faster, as it takes its tensor-core tiles there (32 heads on 8,
+ *    4 bits, the last S of 32768 tokens, whole context: S = 32 351 us over the cache, S = 64 675 us
+ *    and 425 us; window 512: 29, and 40 and 24 us).
  *
  *   gate, gate_mode, sm_scale (<= 0: 1/sqrt(DQK)), out [B,S,H,DV]: as dsa_sparse_attn.  Keys a
  *   query does not see are not read, whatever they hold.  A row without keys (padding, a context
@@ -474,7 +479,9 @@ dsa_status dsa_cache_attn(const dsa_cache* cache, const void* q, const int32_t* 
                           dsa_stream_t stream);
 /* 5d. The same over selected keys: idx [B,S,K] int32 as the top-k gives them (section 2); -1,
  *    entries past pos and tokens without a page are skipped.  A row's valid entries must be
- *    distinct. */
+ *    distinct.  The indexer and the top-k take one T for their whole batch: for sequences of
+ *    different lengths call them once for each (T its length), as keys behind the end of a shorter
+ *    one would otherwise take places of its K and be skipped here. */
 size_t dsa_cache_sparse_attn_workspace_bytes(const dsa_cache* cache, int B, int S, int H, int K);
 dsa_status dsa_cache_sparse_attn(const dsa_cache* cache, const void* q, const int32_t* pos,
                                  const int32_t* idx, int K, const void* gate,

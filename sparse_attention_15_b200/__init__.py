@@ -708,7 +708,8 @@ def _cache_attn(q, cache, pos, idx, window, n_first, gate, gate_mode, sm_scale, 
 def dsa_cache_attn(q, cache, pos, window=0, n_first=0, gate=None, gate_mode=None, sm_scale=0.0,
                    out=None, ws=None, stream=None):
     """Attention of the tokens q [B,S,H,DQK] at pos [B,S] over the cache: every key t <= pos
-    (window 0), or t > pos - window together with t < n_first."""
+    (window 0), or t > pos - window together with t < n_first.  From 64 tokens of a sequence on,
+    dsa_cache_read of what they see and dsa_window_attn are faster."""
     return _cache_attn(q, cache, pos, None, window, n_first, gate, gate_mode, sm_scale, out, ws,
                        stream)
 
@@ -716,5 +717,6 @@ def dsa_cache_attn(q, cache, pos, window=0, n_first=0, gate=None, gate_mode=None
 def dsa_cache_sparse_attn(q, cache, pos, idx, gate=None, gate_mode=None, sm_scale=0.0, out=None,
                           ws=None, stream=None):
     """Attention of the tokens q [B,S,H,DQK] at pos [B,S] over the selected keys idx [B,S,K] of the
-    cache (int32, -1 padded, as dsa_topk and dsa_index_topk give them)."""
+    cache (int32, -1 padded, as dsa_topk and dsa_index_topk give them; those take one length for a
+    batch, so sequences of different lengths are indexed one by one)."""
     return _cache_attn(q, cache, pos, idx, 0, 0, gate, gate_mode, sm_scale, out, ws, stream)

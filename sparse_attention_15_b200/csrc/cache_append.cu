@@ -19,10 +19,13 @@
 // group with one among its x gets a NaN scale and reads back as NaN.  (A finite x whose y is past
 // float32's range saturates like any other.)
 //
-// Memory-bound in bf16 (8192 tokens of 32 heads, 520 MB: 90 us, 5.8 TB/s); in 4 bits (2 x 4001 tokens
-// of 8 heads, 246 MB: 60 us, 4.1 TB/s) latency and the encoding's instructions show.  A thread takes
-// a group of 16 values (32 bytes in, 8 + 1 out, or 32), so a group's maximum needs no exchange; a
-// half-split thread takes both groups of its pairs.
+// Memory-bound in bf16 (8192 tokens of 32 heads, 537 MB: 95 us, 5.7 TB/s; reading back, 335 MB: 56
+// us, 6.0 TB/s).  In 4 bits (2 x 4001 tokens of 8 heads, 249 MB: 60 us, 4.1 TB/s; reading back, 52 MB:
+// 12.5 us, 4.2 TB/s) latency and the encoding's instructions show, and with them the registers: at 64
+// a thread the half-split kernels spill 150 bytes, the interleaved ones 24, and the encoding by
+// division, a call of its own, keeps its group on the stack.  A thread takes a group of 16 values (32
+// bytes in, 8 + 1 out, or 32), so a group's maximum needs no exchange; a half-split thread takes both
+// groups of its pairs.
 #include <math.h>
 
 #include "cache.cuh"
@@ -458,9 +461,12 @@ TensorScale tensor_scale(float scale) {
 }
 
 // Tokens per CTA: enough CTAs to fill the GPU first, then several tokens each (their sines in one
-// go, and their units spread over the warps): four 4-bit tokens (2 x 4001 tokens with reading back:
-// 76 us; two: 81 us; three or six: 86-88 us), two bf16 ones, whose rows are larger (8192: 149 us;
-// four: 155 us).
+// go, and their units spread over the warps).  Appending with queries of 32 heads, in us for one, two,
+// three and four tokens a CTA (interleaved pairs): 4 bits, 8 heads, 4736 tokens 41, 37, 39, 34; 8002
+// tokens 66, 62, 60, 57; 24000 tokens 185, 166, 163, 158: four.  bf16, 32 heads, 8002 tokens 100, 91,
+// 92, 94 and reading back 52, 54, 56, 57; 24000 tokens 286, 258, 259, 259 and 146, 149, 152, 154: two
+// (8 heads would take four: 24000 tokens 184, 165, 151, 150).  The last, partly filled round of CTAs
+// moves any one size by up to 10% either way (4 bits, 6000 tokens: 50, 46, 45, 48).
 int tokens_per_cta(long long tokens, int format) {
   const long long per = tokens / (148 * 8), most = format == 1 ? 4 : 2;
   return (int)(per < 1 ? 1 : (per > most ? most : per));

@@ -21,11 +21,14 @@
 // own head's part of 16 keys at a time into its own ring (cp.async, 16 bytes a lane, a step or two
 // ahead), so the loop has no barrier and no producer.
 //
-// What bounds the 4-bit form: 9/16 byte a value, so at 6.5 TB/s 41 values arrive per clock and SM,
-// and each has to be widened to f16 before the tensor cores take it: about 22 instructions per 256
-// values (16 bytes of codes a thread become 16 f16 pairs by 16 conversions and 16 products with
-// the group's scale).  The issue slots and the bandwidth run out together, so everything else is
-// kept short.  The V operand needs two keys in a register: the nibbles of two keys are interleaved
+// What bounds the 4-bit form: latency, with neither limit reached (64 x 2048 keys: issue slots 62%
+// used, DRAM 50%).  A step (16 keys of a head, 5120 values of 9/16 byte) takes 450 instructions, the
+// pieces' starts and ends counted in: 160 widen (a conversion and a product with the group's scale for
+// each f16 pair, 8 per 256 values), 20 are MMAs, 85 copy and look up, the rest are the softmax, the
+// masks, addresses and the probabilities' pairs.  At 6.5 TB/s 41 values arrive per clock and SM, which
+// would take 3.6 of its 4 issue slots; four warps a scheduler do not cover the widening's chains well
+// enough for that (stalls per issue: fixed latencies 1.6, busy half-rate pipes 0.7).  So everything
+// else is kept short.  The V operand needs two keys in a register: the nibbles of two keys are interleaved
 // before the conversion, which makes pairs of nibbles.  Widening is exact: an e2m1 value times an
 // e4m3 scale has 6 significant bits and stays in f16's normal range.  Queries become f16 after a
 // scaling of each head by a power of two (its largest element to [2^13, 2^14)): exact for every
@@ -36,10 +39,12 @@
 // costs no product (64 x 2048 keys: 206 us, one f16 201 us, two products 219 us).  Warps of 5 to 8
 // heads take two products, as bf16 rows do.
 //
-// Measured: 64 x 2048 selected keys of 32 heads (755 MB) in 180 us, 4.2 TB/s; eight contexts of up to
-// 131072 tokens and 8 heads (1.13 GB) in 250-260 us, 4.4 TB/s.
+// Measured, a call among others: 64 x 2048 selected keys of 32 heads (755 MB) in 199-207 us, 3.7 TB/s;
+// eight contexts of up to 131072 tokens and 8 heads (1.13 GB) in 282-314 us (by where the pages lie),
+// 3.6-4.0 TB/s.  (The figures of the layouts below, taken in a graph on one set of pages, compare with
+// 250-260 us there.)
 //
-// bf16 rows are bound by the bandwidth (16 x 2048 keys of 32 heads, 671 MB: 121 us, 5.5 TB/s).  They
+// bf16 rows are bound by the bandwidth (16 x 2048 keys of 32 heads, 671 MB: 122-128 us, 5.4 TB/s).  They
 // are used as they are; probabilities are a bf16 pair, as one bf16 would be no more exact than the
 // output.
 #include <cuda_fp16.h>
