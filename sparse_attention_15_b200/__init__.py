@@ -572,11 +572,11 @@ class Cache:
         self._pages_at, self._table_at = pages.data_ptr(), table.data_ptr()
         self._B, self._entries = table.shape[0], table.numel()
         self._device_index = self.device.index
-        self._fixed = True
+        self._fixed = frozenset(self.__dict__)
 
     def __setattr__(self, name, value):
         # (the library reads its own copy, `args`: a new table here would not reach it)
-        if "_fixed" in self.__dict__:
+        if name in self.__dict__.get("_fixed", ()):
             raise AttributeError(f"a Cache is not changed ({name}): make a new one")
         object.__setattr__(self, name, value)
 

@@ -197,9 +197,11 @@ def test_a_cache_is_not_changed(answers):
     """Another page table, or other sizes, would not reach the library: they take a new Cache."""
     c, pos = some_cache(), torch.zeros(2, 1, dtype=torch.int32)
     for name, value in (("table", torch.zeros(2, 9, dtype=torch.int32)), ("pages", c.pages.clone()),
-                        ("kv_heads", 1), ("dqk", 128), ("device", "cpu"), ("other", 1)):
+                        ("kv_heads", 1), ("dqk", 128), ("device", "cpu"), ("args", None)):
         with pytest.raises(AttributeError):
             setattr(c, name, value)
+    c.lengths = [3]  # what a program keeps with it is its own
+    c.lengths = [4]
     dsa.dsa_cache_read(c, pos)
     c.table[:] = 3  # the entries may change
     dsa.dsa_cache_read(c, pos)
