@@ -884,6 +884,9 @@ bool make_plan(int format, int rows, int H, int HKV, int DQK, int DV, long long 
   // us, for 2, 4 and 8 steps: one 4-bit window of 33 steps in 2 groups 11.7, 12.7, 16.6; 16 of them
   // 18.0, 15.7, 17.5; one context of 257 steps 21.5, 15.7, 16.9; 20 tokens of 32 steps in 5 groups
   // 23.0, 22.9, 19.1; 8 contexts of 257 steps 28.7, 28.7, 27.1.
+  // Over 72 shapes (both formats, 8 and 32 KV heads, 1 to 64 rows of 64 to 131072 keys) 2 steps
+  // throughout are up to 18 us slower than this rule, 4 up to 14, 8 up to 4, and none is faster by more
+  // than the timer's 2 us; without the whole shares below, 4 us slower at most and 2 faster.
   const long long ctas = (long long)rows * p->nhg;
   const long long steps = ctas * ((max_keys + 16 * p->kw - 1) / (16 * p->kw));
   p->least_log = steps <= 2 * 148 ? 1 : steps <= 8 * 148 ? 2 : 3;
