@@ -39,9 +39,9 @@
 // costs no product (64 x 2048 keys: 206 us, one f16 201 us, two products 219 us).  Warps of 5 to 8
 // heads take two products, as bf16 rows do.
 //
-// Measured, a call among others: 64 x 2048 selected keys of 32 heads (755 MB) in 199-207 us, 3.7 TB/s;
-// eight contexts of up to 131072 tokens and 8 heads (1.13 GB) in 282-314 us (by where the pages lie),
-// 3.6-4.0 TB/s.  (The figures of the layouts below, taken in a graph on one set of pages, compare with
+// Measured, a call among others: 64 x 2048 selected keys of 32 heads (755 MB) in 199-211 us, 3.7 TB/s;
+// eight contexts of up to 131072 tokens and 8 heads (1.13 GB) in 282-333 us (by the machine and
+// where the pages lie), 3.4-4.0 TB/s.  (The figures of the layouts below, taken in a graph on one set of pages, compare with
 // 250-260 us there.)
 //
 // bf16 rows are bound by the bandwidth (16 x 2048 keys of 32 heads, 671 MB: 122-128 us, 5.4 TB/s).  They
