@@ -72,7 +72,7 @@ struct CacheAttnArgs {
   float* part_o;           // [piece, heads of a CTA, DV] (pieces)
   float* part_ml;          // [piece, heads of a CTA, 2]
   int gate_mode, S, H, G, K, window, n_first;
-  float qk_scale;          // sm_scale * log2(e) * k_scale
+  float qk_scale;          // sm_scale * log2(e)
   int rows, hc, nhg;       // query tokens, KV heads per CTA, CTAs per token and step
   int nsub, kw;            // warps per KV head (8 query heads each), 16-key groups side by side
   int grid;                // CTAs that share the steps in pieces; 0: one CTA per token and group
@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(32 * kWarps, (FMT == 1 || Ring<FMT, DQK, DV>::
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = max((int)(top >> 23) - 127, -100);  // 2^ex <= max|q| (or less)
       const float up = __int_as_float((13 - ex + 127) << 23);
-      const float scale = a.qk_scale * __int_as_float((ex - 13 + 127) << 23);
+      // (in this order: the tensor's scale may be as small as q is large)
+      const float scale = a.qk_scale * __int_as_float((ex - 13 + 127) << 23) * a.c.k_scale;
 #pragma unroll
       for (int c = 0; c < QC; ++c)
 #pragma unroll
@@ -996,7 +997,7 @@ cudaError_t launch_cache_attn(const CacheAttnProblem& p, void* ws, size_t ws_byt
   a.gate = static_cast<const __nv_bfloat16*>(p.gate); a.gate_mode = p.gate_mode;
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.S = p.S; a.H = p.H; a.G = p.H / p.cache.HKV; a.rows = p.B * p.S;
-  a.qk_scale = p.sm_scale * kLog2e * p.cache.k_scale;
+  a.qk_scale = p.sm_scale * kLog2e;
   a.hc = pl.hc; a.nhg = pl.nhg; a.nsub = pl.nsub; a.kw = pl.kw; a.grid = pl.grid;
   a.least_log = pl.least_log;
   if (pl.grid > 0) {

@@ -234,3 +234,21 @@ def test_graphs_with_side_streams_and_at_the_same_time(lib, cuda_dev):
     for got, right in zip(held, want):
         for x, y in zip(got, right):
             assert torch.equal(x, y)
+
+
+def test_a_small_key_scale_beside_large_queries(lib, cuda_dev):
+    """Scores of ordinary size from q near 2^128, a key scale of 2^-100 and sm_scale 2^-46, whose product
+    with the key scale alone has 4 bits left in float32: keys of one value each, scores up to 2.
+    (float32: sums of 192 equal products and three scalings, 2^-20 of scores below 2^2 in log2 units.)"""
+    s = Setup(lib, cuda_dev, "e2m1", B=1, ctx=64, page=16, HKV=1, DQK=192, DV=64, k_scale=2.0**-100,
+              fill=False)
+    codes = np.array([0, .5, 1, 1.5, 2, 3, 4, 6, -6, -4, -3, -2, -1.5, -1, -.5, 5.0])
+    k = np.broadcast_to((np.tile(codes, 4) * 448 * 2.0**-100)[None, :, None, None], (1, 64, 1, 192))
+    v = s.normal(1, 64, 1, 64)
+    every = torch.arange(64, dtype=torch.int32, device=cuda_dev)[None]
+    lib.dsa_cache_append(s.cache, every, s.cuda(k.copy()), s.cuda(v))
+    for t in range(64):
+        _, s.k[0, t], s.v[0, t] = O.row_of(O.to_bf16(k[0, t]), v[0, t], "e2m1", 2.0**-100, 1.0)
+    q, sm = np.full((4, 192), 1.75 * 2.0**127), 2.0**-46
+    out = lib.dsa_cache_attn(s.cuda(q[None, None]), s.cache, every[:, -1:].contiguous(), sm_scale=sm)
+    check(out[0, 0], *O.attend(q, s.k[0], s.v[0], list(range(64)), sm))
